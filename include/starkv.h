@@ -415,6 +415,148 @@ STARKV_API starkv_status starkv_hybrid_decode(const starkv_layout* lay, const vo
                                               float* out, void* workspace, size_t workspace_bytes,
                                               int32_t* dev_status, starkv_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The plain (full-rank) key-value cache: layers that stay uncompressed, or a whole model
+ * beside the compressed one.  Keys are stored after the position rotation, values as they
+ * are, in the same 64-token pages and block tables as the latent cache.  (The pages describe
+ * no such cache; it is the form their method compresses.)
+ *
+ * A decode step: starkv_kv_append (rotates q and k, stores k and v), then starkv_kv_decode
+ * over the whole sequence, or starkv_kv_select and starkv_kv_decode over the pages it chose. */
+typedef enum {
+  STARKV_KV_BF16 = 0, /* q, k, v and results bf16; stored as they are                        */
+  STARKV_KV_F16 = 1,  /* the same in fp16                                                    */
+  STARKV_KV_INT8 = 2  /* q, k, v and results bf16; stored as int8 codes with one fp16 scale
+                         per token and group of 32 channels: the quantiser of the int8 part
+                         of STARKV_FMT_MIXED, applied to the fp32 rotated key and to the
+                         value.  Values above 65504 in magnitude are not representable       */
+} starkv_kv_fmt;
+
+typedef struct {
+  int32_t n_q_heads;   /* H; a multiple of n_kv_heads, at most 64 per KV head                */
+  int32_t n_kv_heads;  /* H_kv, 1..STARKV_MAX_KV_HEADS                                       */
+  int32_t head_dim;    /* d: 64 or 128                                                       */
+  int32_t fmt;         /* starkv_kv_fmt                                                      */
+  int32_t page_tokens; /* must be 64                                                         */
+  int32_t reserved;    /* 0                                                                  */
+  double rope_theta;   /* base of the rotation, > 1                                          */
+} starkv_kv_config;
+
+/* A page: the bounds of its keys [H_kv][2][d] (16 bits each: per channel the smallest and the
+ * largest stored key of the page, in the type of k), then per KV head a tile of head_bytes:
+ * keys [64][d], values [64][d] and, for int8, the keys' scales [64][d/32] and the values'. */
+typedef struct {
+  starkv_kv_config cfg;
+  int64_t page_bytes;  /* a multiple of 16                                                   */
+  int64_t token_bytes; /* stored bytes per token, keys and values of all heads, no bounds    */
+  int64_t off_heads;   /* first tile = bytes of the bounds                                   */
+  int64_t head_bytes;  /* one tile                                                           */
+  int64_t off_v;       /* inside a tile: values                                              */
+  int64_t off_ks;      /* inside a tile: scales of the keys (-1 without)                     */
+  int64_t off_vs;      /* inside a tile: scales of the values (-1 without)                   */
+} starkv_kv_layout;
+
+typedef struct {
+  size_t cache_bytes;            /* num_pages * page_bytes                                   */
+  size_t rope_table_bytes;       /* table for positions < max_pages * 64                     */
+  size_t decode_workspace_bytes; /* partial records of one decode call, any batch and length */
+} starkv_kv_sizes;
+
+/* Host only, pure. */
+STARKV_API starkv_status starkv_kv_layout_init(const starkv_kv_config* cfg, starkv_kv_layout* out);
+STARKV_API starkv_status starkv_kv_alloc(const starkv_kv_layout* lay, int64_t num_pages,
+                                         int32_t max_pages, starkv_kv_sizes* out);
+
+/* The table of starkv_rope_init for this layout's head_dim and rope_theta. */
+STARKV_API starkv_status starkv_kv_rope_init(const starkv_kv_layout* lay, int32_t max_pages,
+                                             void* table, size_t table_bytes,
+                                             starkv_stream_t stream);
+
+/* Rotate and store the keys and values of new tokens, and rotate their queries.
+ *   q, k, v     device, token n's heads at q + n * q_stride ([H][d]; k, v [H_kv][d]); strides in
+ *               elements, at least the row and a multiple of 8 (slices of one fused projection);
+ *               q NULL (with q_out NULL): keys and values only
+ *   tok_seq/pos, block_table, cache: as starkv_quant_pack.  Tokens of one call are distinct
+ *   rope_table  from starkv_kv_rope_init with max_pages >= this call's max_pages
+ *   q_out       device [n_tok][H][d]: the rotated queries, rounded once; may be q itself where
+ *               q_stride is H d
+ * Angles are pos * theta^(-2j/d); the products run in fp32 and each result is rounded once
+ * (int8: quantised from fp32).  A token in slot 63 completes its page: the call writes the
+ * page's bounds from its 64 stored keys, whichever call stored them.  A page that is not
+ * complete has no valid bounds (starkv_kv_select reads none: it always takes the last pages);
+ * a caller that rewrites earlier tokens of a complete page appends its slot 63 again.
+ * Tokens with a bad sequence, position or page are skipped and flagged STARKV_DEV_BOUNDS; their
+ * q_out rows are still rotated when the position lies inside the block table, else zero. */
+STARKV_API starkv_status starkv_kv_append(
+    const starkv_kv_layout* lay, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+    const void* v, int64_t v_stride, int32_t n_tok, const int32_t* tok_seq, const int32_t* tok_pos,
+    const int32_t* block_table, int32_t max_pages, int32_t batch, const void* rope_table,
+    size_t rope_table_bytes, void* cache, int64_t num_pages, void* q_out, int32_t* dev_status,
+    starkv_stream_t stream);
+
+/* Read stored tokens back: k_out, v_out device [n_tok][H_kv][d] in the type of k (int8: code
+ * times scale, rounded).  Tokens with a bad page or position give zeros and are flagged. */
+STARKV_API starkv_status starkv_kv_gather(const starkv_kv_layout* lay, const void* cache,
+                                          int64_t num_pages, const int32_t* tok_seq,
+                                          const int32_t* tok_pos, int32_t n_tok,
+                                          const int32_t* block_table, int32_t max_pages,
+                                          int32_t batch, void* k_out, void* v_out,
+                                          int32_t* dev_status, starkv_stream_t stream);
+
+/* Choose pages for sparse attention.  For KV head g and a complete page p,
+ *   score(g, p) = max over the query heads h of g of sum_c max(q_h,c lo_p,c, q_h,c hi_p,c),
+ * an upper bound of every q_h . k_t in the page, summed in fp64 so that the order of pages does
+ * not hang on rounding.  A sequence of P = ceil(seq_len / 64) pages gets all of them when
+ * P <= n_sel; else its first keep_first and last keep_last pages and, of the rest, those of
+ * the largest score (equal scores: the lower page first), n_sel in all.
+ *   q        device [batch][H][d], rotated (q_out of the append)
+ *   sel      device int32 [batch][H_kv][n_sel]: page indices of the sequence, ascending; unused
+ *            places -1
+ * Needs 1 <= keep_last (the last page has no bounds yet), 0 <= keep_first,
+ * keep_first + keep_last <= n_sel, and max_pages <= STARKV_KV_MAX_SELECT_PAGES.  Bounds that hold
+ * an infinity or NaN give an unspecified choice (of valid pages).  A bad block-table entry is
+ * flagged and its page takes the lowest score. */
+#define STARKV_KV_MAX_SELECT_PAGES 16384
+STARKV_API starkv_status starkv_kv_select(const starkv_kv_layout* lay, const void* q,
+                                          const void* cache, int64_t num_pages,
+                                          const int32_t* block_table, int32_t max_pages,
+                                          const int32_t* seq_lens, int32_t batch, int32_t n_sel,
+                                          int32_t keep_first, int32_t keep_last, int32_t* sel,
+                                          int32_t* dev_status, starkv_stream_t stream);
+
+/* Settings of starkv_kv_decode (NULL = defaults). */
+typedef struct {
+  float scale;      /* of the scores; 0 = 1 / sqrt(d)                                        */
+  int32_t window;   /* attend the last `window` tokens only; 0 = all                         */
+  int32_t max_ctas; /* CTAs of the split kernel; 0 = as many as fit on the device            */
+  int32_t reserved; /* 0                                                                     */
+} starkv_kv_decode_opts;
+
+/* Attention of one token per sequence: softmax(scale q_h . k_t) over the tokens t < seq_len of
+ * the cache, times their values.
+ *   q         device [batch][H][d], rotated (q_out of the append)
+ *   sel       device int32 [batch][H_kv][n_sel] from starkv_kv_select, or NULL for all pages;
+ *             places are read up to min(P, n_sel), an entry of -1 is skipped, one outside the
+ *             sequence is flagged and skipped, one that stands twice counts twice.  Not together
+ *             with a window (INVALID_ARG)
+ *   out       device [batch][H][d] in the type of q
+ *   lse       device fp32 [batch][H]: ln sum_t exp(scale q_h . k_t), or NULL
+ *   workspace device, >= decode_workspace_bytes; two calls that may overlap on the GPU need two
+ * An empty sequence gives zeros and -inf.  Tokens of a bad block-table entry are flagged and
+ * skipped; a seq_len above max_pages * 64 is flagged and cut.  Rows of the last page behind the
+ * sequence, and before the window, are never read into a sum, whatever they hold; an infinite
+ * value that does count gives an infinity or a NaN in its channel.
+ * Two launches: a split kernel, whose CTAs take equal shares of all pages of the batch, and a
+ * join of the sequences that were split.  Results do not depend on timing. */
+STARKV_API starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q,
+                                          const void* cache, int64_t num_pages,
+                                          const int32_t* block_table, int32_t max_pages,
+                                          const int32_t* seq_lens, int32_t batch,
+                                          const int32_t* sel, int32_t n_sel,
+                                          const starkv_kv_decode_opts* opts, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes,
+                                          int32_t* dev_status, starkv_stream_t stream);
+
 /* Failure-detection check of the in-kernel bounded waits: one CTA holds TMEM and waits on a
  * barrier that nothing completes.  After ``timeout_ms`` (1..10000) the wait gives up, the CTA
  * sets STARKV_DEV_TIMEOUT in *dev_status, releases TMEM and returns; the context stays usable.

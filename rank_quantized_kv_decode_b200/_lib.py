@@ -14,6 +14,8 @@ TILE_TOKENS = 128
 
 FMT = {"f32": 0, "bf16": 1, "mixed": 2, "had43": 3}
 ASSIGN_JOINT_KEYS, ASSIGN_HYBRID = 0, 1
+KV_FMT = {"bf16": 0, "f16": 1, "int8": 2}
+KV_MAX_SELECT_PAGES = 16384
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 0, 1, 2, 3, 4
 DEV_BOUNDS, DEV_TIMEOUT = 1, 2
@@ -62,6 +64,24 @@ class DecodePlan(ctypes.Structure):
                 ("grid", i32), ("work_units", i32)]
 
 
+class KvConfig(ctypes.Structure):
+    _fields_ = [("n_q_heads", i32), ("n_kv_heads", i32), ("head_dim", i32), ("fmt", i32),
+                ("page_tokens", i32), ("reserved", i32), ("rope_theta", f64)]
+
+
+class KvLayout(ctypes.Structure):
+    _fields_ = [("cfg", KvConfig), ("page_bytes", i64), ("token_bytes", i64), ("off_heads", i64),
+                ("head_bytes", i64), ("off_v", i64), ("off_ks", i64), ("off_vs", i64)]
+
+
+class KvSizes(ctypes.Structure):
+    _fields_ = [("cache_bytes", sz), ("rope_table_bytes", sz), ("decode_workspace_bytes", sz)]
+
+
+class KvDecodeOpts(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("window", i32), ("max_ctas", i32), ("reserved", i32)]
+
+
 EXPORTS = {
     "starkv_layout_init": (i32, [ctypes.POINTER(Config), ctypes.POINTER(Layout)]),
     "starkv_hybrid_layout_init": (i32, [ctypes.POINTER(HybridConfig), ctypes.POINTER(Layout)]),
@@ -91,6 +111,17 @@ EXPORTS = {
     "starkv_absorb_output_weights": (i32, [ctypes.POINTER(Layout), vp, vp, i32, vp, vp]),
     "starkv_decode_combine_absorbed": (i32, [ctypes.POINTER(Layout), vp, i32, i32, vp, i32, vp, sz,
                                              vp, sz, vp, vp]),
+    "starkv_kv_layout_init": (i32, [ctypes.POINTER(KvConfig), ctypes.POINTER(KvLayout)]),
+    "starkv_kv_alloc": (i32, [ctypes.POINTER(KvLayout), i64, i32, ctypes.POINTER(KvSizes)]),
+    "starkv_kv_rope_init": (i32, [ctypes.POINTER(KvLayout), i32, vp, sz, vp]),
+    "starkv_kv_append": (i32, [ctypes.POINTER(KvLayout), vp, i64, vp, i64, vp, i64, i32, vp, vp, vp,
+                               i32, i32, vp, sz, vp, i64, vp, vp, vp]),
+    "starkv_kv_gather": (i32, [ctypes.POINTER(KvLayout), vp, i64, vp, vp, i32, vp, i32, i32, vp, vp,
+                               vp, vp]),
+    "starkv_kv_select": (i32, [ctypes.POINTER(KvLayout), vp, vp, i64, vp, i32, vp, i32, i32, i32,
+                               i32, vp, vp, vp]),
+    "starkv_kv_decode": (i32, [ctypes.POINTER(KvLayout), vp, vp, i64, vp, i32, vp, i32, vp, i32,
+                               ctypes.POINTER(KvDecodeOpts), vp, vp, vp, sz, vp, vp]),
     "starkv_diag_bounded_wait": (i32, [i32, vp, vp]),
     "starkv_last_error": (ctypes.c_char_p, []),
     "starkv_version": (i32, []),

@@ -300,6 +300,143 @@ def decode_combine_absorbed(lay, seq_lens, max_pages: int, M, workspace, scratch
         "starkv_decode_combine_absorbed")
 
 
+# ---- the plain (full-rank) key-value cache
+_KV_DTYPE = {L.KV_FMT["bf16"]: torch.bfloat16, L.KV_FMT["f16"]: torch.float16,
+             L.KV_FMT["int8"]: torch.bfloat16}
+
+
+def make_kv_config(n_q_heads: int, n_kv_heads: int, head_dim: int, fmt: str, rope_theta: float,
+                   page_tokens: int = 64) -> L.KvConfig:
+    """Config of a plain cache: ``fmt`` "bf16", "f16" or "int8" (int8 codes of bf16 keys and values)."""
+    return L.KvConfig(n_q_heads, n_kv_heads, head_dim, L.KV_FMT[fmt], page_tokens, 0, float(rope_theta))
+
+
+def kv_layout_init(cfg: L.KvConfig) -> L.KvLayout:
+    lay = L.KvLayout()
+    L.check(L.load().starkv_kv_layout_init(ctypes.byref(cfg), ctypes.byref(lay)), "starkv_kv_layout_init")
+    return lay
+
+
+def kv_alloc(lay: L.KvLayout, num_pages: int, max_pages: int) -> L.KvSizes:
+    s = L.KvSizes()
+    L.check(L.load().starkv_kv_alloc(ctypes.byref(lay), num_pages, max_pages, ctypes.byref(s)),
+            "starkv_kv_alloc")
+    return s
+
+
+def kv_rope_init(lay: L.KvLayout, max_pages: int, table: torch.Tensor, stream=None) -> None:
+    L.check(L.load().starkv_kv_rope_init(ctypes.byref(lay), max_pages, _ptr(table),
+                                         table.numel() * table.element_size(), _stream(stream)),
+            "starkv_kv_rope_init")
+
+
+def _check_kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int) -> None:
+    """[n_tok][heads][d]; a token's heads are contiguous, the tokens may be slices of wider rows."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.shape[0] < n_tok:
+        raise ValueError(f"{name}: expected shape ({n_tok}, {heads}, {d}), got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+
+
+def _kv_rows(t) -> tuple[int | None, int]:
+    """Pointer and token stride of such a tensor."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.device.index is not None and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _kv_pages(lay, cache) -> int:
+    return cache.numel() * cache.element_size() // lay.page_bytes
+
+
+def _check_kv_batch(lay, q, block_table, seq_lens, status) -> int:
+    c = lay.cfg
+    _need(seq_lens, "seq_lens", torch.int32, ndim=1)
+    _need(block_table, "block_table", torch.int32, ndim=2)
+    batch = seq_lens.shape[0]
+    if block_table.shape[0] < batch:
+        raise ValueError(f"block_table: {block_table.shape[0]} rows for {batch} sequences")
+    _need(q, "q", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim)
+    _need(status, "status", torch.int32, 1)
+    return batch
+
+
+def _check_kv_sel(lay, sel, batch: int) -> int:
+    _need(sel, "sel", torch.int32, ndim=3)
+    if sel.shape[0] < batch or sel.shape[1] != lay.cfg.n_kv_heads:
+        raise ValueError(f"sel: expected ({batch}, {lay.cfg.n_kv_heads}, pages), got {tuple(sel.shape)}")
+    return sel.shape[2]
+
+
+def kv_append(lay, k, v, tok_seq, tok_pos, block_table, cache, rope_table, status, q=None, q_out=None,
+              stream=None) -> None:
+    """Rotate and store keys and values [n][H_kv][d] of new tokens (slices of a fused projection
+    will do), update the bounds of the pages they complete, and rotate their queries into q_out."""
+    c = lay.cfg
+    dt, n_tok = _KV_DTYPE[c.fmt], k.shape[0]
+    _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
+    _need(q_out, "q_out", dt, n_tok * c.n_q_heads * c.head_dim)
+    _check_kv_rows(q, "q", dt, n_tok, c.n_q_heads, c.head_dim)
+    _check_kv_rows(k, "k", dt, n_tok, c.n_kv_heads, c.head_dim)
+    _check_kv_rows(v, "v", dt, n_tok, c.n_kv_heads, c.head_dim)
+    (qp, qs), (kp, ks), (vp, vs) = _kv_rows(q), _kv_rows(k), _kv_rows(v)
+    L.check(L.load().starkv_kv_append(
+        ctypes.byref(lay), qp, qs, kp, ks, vp, vs, n_tok, _ptr(tok_seq), _ptr(tok_pos),
+        _ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(rope_table),
+        rope_table.numel() * rope_table.element_size(), _ptr(cache), _kv_pages(lay, cache),
+        _ptr(q_out), _ptr(status), _stream(stream)), "starkv_kv_append")
+
+
+def kv_gather(lay, cache, tok_seq, tok_pos, block_table, k_out, v_out, status, stream=None) -> None:
+    """Stored keys (rotated) and values of tokens, [n][H_kv][d]."""
+    c = lay.cfg
+    n_tok = tok_seq.shape[0]
+    _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
+    _need(k_out, "k_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
+    _need(v_out, "v_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
+    L.check(L.load().starkv_kv_gather(
+        ctypes.byref(lay), _ptr(cache), _kv_pages(lay, cache), _ptr(tok_seq), _ptr(tok_pos), n_tok,
+        _ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(k_out), _ptr(v_out),
+        _ptr(status), _stream(stream)), "starkv_kv_gather")
+
+
+def kv_select(lay, q, cache, block_table, seq_lens, sel, status, keep_first: int = 0,
+              keep_last: int = 1, stream=None) -> None:
+    """Choose sel.shape[2] pages per sequence and KV head into sel [batch][H_kv][pages]."""
+    batch = _check_kv_batch(lay, q, block_table, seq_lens, status)
+    n_sel = _check_kv_sel(lay, sel, batch)
+    L.check(L.load().starkv_kv_select(
+        ctypes.byref(lay), _ptr(q), _ptr(cache), _kv_pages(lay, cache), _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), batch, n_sel, keep_first, keep_last, _ptr(sel),
+        _ptr(status), _stream(stream)), "starkv_kv_select")
+
+
+def kv_decode(lay, q, cache, block_table, seq_lens, out, workspace, status, sel=None, lse=None,
+              scale: float = 0.0, window: int = 0, max_ctas: int = 0, stream=None) -> None:
+    """Attention of one (rotated) token per sequence over its cached tokens, or over the pages of
+    ``sel``."""
+    c = lay.cfg
+    batch = _check_kv_batch(lay, q, block_table, seq_lens, status)
+    _need(out, "out", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim)
+    _need(lse, "lse", torch.float32, batch * c.n_q_heads)
+    n_sel = _check_kv_sel(lay, sel, batch) if sel is not None else 0
+    opts = L.KvDecodeOpts(scale, window, max_ctas, 0)
+    L.check(L.load().starkv_kv_decode(
+        ctypes.byref(lay), _ptr(q), _ptr(cache), _kv_pages(lay, cache), _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), batch, _ptr(sel), n_sel, ctypes.byref(opts), _ptr(out),
+        _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+        _stream(stream)), "starkv_kv_decode")
+
+
 def diag_bounded_wait(timeout_ms: int, status, stream=None) -> None:
     L.check(L.load().starkv_diag_bounded_wait(timeout_ms, _ptr(status), _stream(stream)),
             "starkv_diag_bounded_wait")
@@ -335,4 +472,28 @@ class LatentCache:
                 _bytes(s.decode_workspace_bytes, device), _bytes(s.append_workspace_bytes, device),
                 torch.zeros(1, dtype=torch.int32, device=device))
         rope_init(lay, max_pages, c.rope)
+        return c
+
+
+@dataclass
+class KvCache:
+    """Caller-side buffers of one layer's plain cache, sized by ``starkv_kv_alloc``."""
+
+    layout: L.KvLayout
+    num_pages: int
+    batch: int
+    max_pages: int
+    cache: torch.Tensor
+    rope: torch.Tensor
+    decode_ws: torch.Tensor
+    status: torch.Tensor
+
+    @classmethod
+    def create(cls, lay: L.KvLayout, num_pages: int, batch: int, max_pages: int,
+               device="cuda") -> "KvCache":
+        s = kv_alloc(lay, num_pages, max_pages)
+        c = cls(lay, num_pages, batch, max_pages, _bytes(s.cache_bytes, device),
+                _bytes(s.rope_table_bytes, device), _bytes(s.decode_workspace_bytes, device),
+                torch.zeros(1, dtype=torch.int32, device=device))
+        kv_rope_init(lay, max_pages, c.rope)
         return c

@@ -14,7 +14,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["api.cu", "decode.cu", "store.cu", "project.cu", "append_gemv.cu", "decode_noalloc.cu",
-           "diag.cu", "absorb.cu", "hybrid.cu"]
+           "diag.cu", "absorb.cu", "hybrid.cu", "kv_api.cu", "kv_append.cu", "kv_select.cu", "kv_decode.cu"]
 LIB = os.path.join(HERE, "libstarkv.so")
 
 

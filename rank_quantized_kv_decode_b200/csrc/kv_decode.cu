@@ -1,0 +1,661 @@
+// Decode attention over the plain key-value cache: a split kernel and a join.
+//
+// Mathematics, per query head: s_t = scale q.k_t, o = sum_t e^{s_t} v_t / sum_t e^{s_t}, in one pass
+// with a running reference m (log2 units): p_t = 2^{s_t log2e - m}, l = sum p_t, O = sum p_t v_t in
+// fp32; raising m multiplies l and O by 2^{m_old - m_new}.  Parts of a sequence join by
+// M = max m_i, l = sum l_i 2^{m_i - M}, O likewise.
+//
+// Bound: HBM.  Every byte of the visited keys and values is read once (for up to eight query heads
+// per KV head), 4 FLOP per byte and query head at 16 bits; the products run on mma.sync
+// m16n8k16, whose 16 rows hold the query heads in the upper half.  For P.V the lower half holds what the
+// weights lost in rounding to 16 bits (p = hi + lo), so that the weights count with 16 bits of mantissa
+// (bf16) or 22 (fp16) at no further instruction.  tcgen05 would give the same products of 8 rows a
+// 128-row tile.
+//
+// Split: all (sequence, KV head, page) units of the batch form one list, and CTA i of N takes the
+// units [T i / N, T (i + 1) / N): equal shares whatever the lengths, known on the device alone.  A
+// CTA walks its share segment by segment (a segment = its part of one sequence and KV head); each
+// of its four warps takes 16 of a page's 64 tokens through a private cp.async ring, so that the
+// loads never wait for another warp.  A segment that is a whole sequence is written out at once,
+// else as a partial record, and the join adds the records of a sequence in page order.
+#include "kv.cuh"
+
+namespace starkv {
+namespace {
+
+constexpr int kWarpTok = kPage / kKvWarps;  // 16: tokens of a warp's tile
+constexpr float kLazy = 8.f;  // the reference follows the running maximum when that is 2^8 above it:
+                              // weights stay below 2^8, and O is rescaled a few times per sequence
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Weights of fp16 products are scaled by 2^7 (the factor is part of the reference): with kLazy they
+// stay below 2^15, and fp16's subnormals begin 2^-21 below the maximum instead of 2^-14.
+template <int FMT>
+constexpr float kShift = FMT == STARKV_KV_BF16 ? 0.f : 7.f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+
+// 16 bytes global -> shared; zeros when not `on` (the address is not read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ------------------------------------------------------------------ shape of a warp's ring
+template <int FMT, int D>
+struct Ring {
+  static constexpr bool kInt8 = FMT == STARKV_KV_INT8;
+  static constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a token's keys (or values)
+  static constexpr int kKeys = kWarpTok * kRow;             // one tile's keys
+  static constexpr int kScales = kInt8 ? kWarpTok * (D / 32) * 2 : 0;
+  static constexpr int kStage = 2 * kKeys + 2 * kScales;
+  // two CTAs per SM (8 warps): about 96 KB of ring per CTA
+  static constexpr int kStages = (kInt8 ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6));
+  static constexpr int kBytes = kStage * kStages;
+};
+template <int FMT, int D>
+constexpr int smem_bytes() {
+  return kKvWarps * Ring<FMT, D>::kBytes + kKvWarps * kKvRows * D * 4 + kKvWarps * kKvRows * 8;
+}
+
+// Offset of a 16-byte chunk of a tile's row in shared memory: the chunks are permuted so that the
+// fragment loads touch every bank once.
+template <bool INT8, int D>
+__device__ __forceinline__ int chunk_at(int row, int c) {
+  if (!INT8) return row * 2 * D + ((c ^ (row & 7)) << 4);
+  if (D == 128) return row * D + (((c >> 1) ^ ((row ^ (row >> 1)) & 3)) << 5) + ((c & 1) << 4);
+  return row * D + (((c >> 1) ^ ((row >> 1) & 1)) << 5) + ((c & 1) << 4);
+}
+
+// ------------------------------------------------------------------ the list of units
+// Pages of a sequence that a call visits: [first, first + count) of the sequence, or count places
+// of its selection.
+struct Span {
+  int len, first, count;
+};
+__device__ __forceinline__ Span span_of(const KvDecodeParams& p, int b) {
+  Span s;
+  s.len = min(max(p.seq_lens[b], 0), p.pool.max_pages * kPage);
+  const int pages = (s.len + kPage - 1) / kPage;
+  s.first = p.window > 0 ? max(0, s.len - p.window) / kPage : 0;
+  s.count = p.sel ? min(pages, p.n_sel) : pages - s.first;
+  return s;
+}
+
+// Sum over the batch of the visited pages, and the part of it before sequence `stop` (whole warp).
+__device__ __forceinline__ long long sum_pages(const KvDecodeParams& p, int lane, int stop, long long& before) {
+  long long all = 0, part = 0;
+  for (int b = lane; b < p.pool.batch; b += 32) {
+    const int c = span_of(p, b).count;
+    all += c;
+    if (b < stop) part += c;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    part += __shfl_xor_sync(0xffffffffu, part, o);
+  }
+  before = part;
+  return all;
+}
+
+// A place in the list: sequence, KV head (and group of its query heads), page of the span.
+struct Cursor {
+  int b, hv, pg;
+  Span s;
+  __device__ __forceinline__ void next_segment(const KvDecodeParams& p, int heads) {
+    pg = 0;
+    if (++hv < heads) return;
+    hv = 0;
+    do {
+      ++b;
+      if (b >= p.pool.batch) return;
+      s = span_of(p, b);
+    } while (s.count == 0);
+  }
+  __device__ __forceinline__ void next(const KvDecodeParams& p, int heads) {
+    if (++pg == s.count) next_segment(p, heads);
+  }
+};
+
+// Place of unit u (whole warp; u below the total).
+__device__ __forceinline__ Cursor find(const KvDecodeParams& p, int lane, int heads, long long u) {
+  Cursor c;
+  long long before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int b = b0 + lane;
+    const int n = b < p.pool.batch ? span_of(p, b).count : 0;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, (before + inc) * heads > u);
+    if (m || b0 + 32 >= p.pool.batch) {
+      const int l = m ? __ffs(m) - 1 : 0;
+      c.b = b0 + l;
+      const long long start = (before + __shfl_sync(0xffffffffu, inc - n, l)) * heads;
+      c.s = span_of(p, c.b);
+      const long long in = u - start;
+      c.hv = static_cast<int>(in / max(c.s.count, 1));
+      c.pg = static_cast<int>(in % max(c.s.count, 1));
+      return c;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
+// ------------------------------------------------------------------ loads
+// Where the warp's tile of the unit at a cursor lies, and which of its rows count: [lo, hi).
+struct Tile {
+  const uint8_t* src;  // the head's tile of the page, or null
+  int lo, hi;
+};
+__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Cursor& c, int warp) {
+  Tile t{nullptr, 0, 0};
+  const int g = c.hv / p.groups;
+  int i = c.s.first + c.pg;
+  if (p.sel) {
+    i = p.sel[((long long)c.b * p.pool.Hkv + g) * p.n_sel + c.pg];
+    if (i == -1) return t;
+    if (i < 0 || i >= (c.s.len + kPage - 1) / kPage) {
+      atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+      return t;
+    }
+  }
+  uint8_t* page = kv_page(p.pool, c.b, i);
+  if (!page) {
+    atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+    return t;
+  }
+  t.src = page + p.pool.off_heads + (long long)g * p.pool.head_bytes;
+  const int t0 = i * kPage + warp * kWarpTok;
+  t.hi = min(max(c.s.len - t0, 0), kWarpTok);
+  t.lo = p.window > 0 ? min(max(c.s.len - p.window - t0, 0), kWarpTok) : 0;
+  return t;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void load_tile(const KvDecodeParams& p, const Tile& t, uint32_t stage, int warp, int lane) {
+  using R = Ring<FMT, D>;
+  constexpr int CPR = R::kRow / 16, N = kWarpTok * CPR;
+  const uint8_t* k = t.src + warp * R::kKeys;
+  const uint8_t* v = k + p.pool.off_v;
+#pragma unroll
+  for (int i = lane; i < N; i += 32) {
+    const int row = i / CPR, at = chunk_at<R::kInt8, D>(row, i % CPR);
+    const bool on = row >= t.lo && row < t.hi;
+    cp16(stage + at, k + i * 16, on);
+    cp16(stage + R::kKeys + at, v + i * 16, on);
+  }
+  if constexpr (R::kInt8) {
+    constexpr int SC = R::kScales / 16;  // 16-byte chunks of a tile's scales (several tokens each)
+    if (lane < 2 * SC) {
+      const int which = lane / SC, i = lane % SC;
+      cp16(stage + 2 * R::kKeys + lane * 16,
+           t.src + (which ? p.pool.off_vs : p.pool.off_ks) + warp * R::kScales + i * 16, true);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ one warp's running sums
+template <int FMT, int D>
+struct Sums {
+  static constexpr bool kInt8 = FMT == STARKV_KV_INT8;
+  static constexpr bool kBf = FMT == STARKV_KV_BF16;
+  uint32_t q[D / 16][2];  // A fragments of the queries: rows 0..7 (the lower half is zero)
+  float qs;               // factor of the dot products: scale log2(e), int8: times the query's power of two
+  float o[D / 8][4];      // O: [0,1] of the weights' high part, [2,3] of the low part
+  float m, l;             // of row lane / 4; l is this lane's share
+
+  __device__ __forceinline__ void begin(const KvDecodeParams& p, int b, int hv, int lane) {
+    const int g = hv / p.groups, G = p.pool.H / p.pool.Hkv;
+    const int row = hv % p.groups * kKvRows + lane / 4, t = lane % 4;
+    const bool in = row < G;
+    const uint16_t* src = p.q + ((long long)b * p.pool.H + g * G + (in ? row : 0)) * D;
+    qs = p.scale2;
+    if (!kInt8) {
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          q[s][i] = in ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * i + 2 * t) : 0u;
+    } else {
+      // fp16 queries: scaled by a power of two to a magnitude near 1, so that bf16's eight bits are
+      // exact down to 2^-16 of the largest.  Channels 32 j + 8 t + (0..7) of scale group j.
+      float x[D / 32][8], mx = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src + 32 * j + 8 * t);
+        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = kv_unpack<STARKV_KV_BF16>(a[i]);
+          x[j][2 * i] = in ? f.x : 0.f, x[j][2 * i + 1] = in ? f.y : 0.f;
+          mx = fmaxf(mx, fmaxf(fabsf(x[j][2 * i]), fabsf(x[j][2 * i + 1])));
+        }
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = min(max(__float_as_int(mx) >> 23, 1), 253);
+      const float down = __int_as_float((254 - e) << 23);
+      qs *= __int_as_float(e << 23);
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[2 * j + i / 2][i % 2] = kv_pack<STARKV_KV_F16>(x[j][2 * i] * down, x[j][2 * i + 1] * down);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m = __int_as_float(0xff800000);
+    l = 0.f;
+  }
+
+  // Scores (dot products) of the tile's tokens 2t, 2t+1, 8+2t, 9+2t for row lane / 4.
+  __device__ __forceinline__ void scores(uint32_t stage, int lane, float (&s)[4]) const {
+    using R = Ring<FMT, D>;
+    if (!kInt8) {
+      float c[2][4] = {};
+      const int mi = lane / 8, row = lane % 8 + 8 * (mi >> 1);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t f[4];
+        ldsm4(f, stage + chunk_at<false, D>(row, 2 * k + (mi & 1)));
+        mma16816<kBf>(c[0], q[k][0], 0u, q[k][1], 0u, f[0], f[1]);
+        mma16816<kBf>(c[1], q[k][0], 0u, q[k][1], 0u, f[2], f[3]);
+      }
+      s[0] = c[0][0], s[1] = c[0][1], s[2] = c[1][0], s[3] = c[1][1];
+    } else {
+      const int g = lane / 4, t = lane % 4;
+      const uint32_t sc = stage + 2 * R::kKeys;
+      s[0] = s[1] = s[2] = s[3] = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        // the fp32 scales of this lane's two result columns
+        float f[2][D / 32];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) {
+            const uint32_t w = ld_shared_u32(sc + (8 * half + 2 * t + i) * (D / 16) + 4 * j);
+            const float2 x = kv_unpack<STARKV_KV_F16>(w);
+            f[i][2 * j] = x.x, f[i][2 * j + 1] = x.y;
+          }
+        const int row = g + 8 * half;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint2 w = ld_shared_v2(stage + chunk_at<true, D>(row, 2 * j) + 8 * t);
+          uint32_t h[4];
+          halves(w.x, h[0], h[1]);
+          halves(w.y, h[2], h[3]);
+          float c[4] = {};
+          mma16816<false>(c, q[2 * j][0], 0u, q[2 * j][1], 0u, h[0], h[1]);
+          mma16816<false>(c, q[2 * j + 1][0], 0u, q[2 * j + 1][1], 0u, h[2], h[3]);
+          s[2 * half] = fmaf(c[0], f[0][j], s[2 * half]);
+          s[2 * half + 1] = fmaf(c[1], f[1][j], s[2 * half + 1]);
+        }
+      }
+    }
+  }
+
+  // Four codes as fp16 pairs, exact: code + 128 under the exponent of 1024, minus 1152.
+  static __device__ __forceinline__ uint32_t less1152(uint32_t w) {
+    const __half2 k = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), k);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ void halves(uint32_t codes, uint32_t& a, uint32_t& b) {
+    const uint32_t u = codes ^ 0x80808080u;
+    a = less1152(__byte_perm(u, 0x64646464u, 0x4140));
+    b = less1152(__byte_perm(u, 0x64646464u, 0x4342));
+  }
+
+  // Adds the tile's rows [lo, hi) of keys and values at `stage`.
+  __device__ __forceinline__ void add(uint32_t stage, int lo, int hi, int lane) {
+    using R = Ring<FMT, D>;
+    const int t = lane % 4;
+    float s[4];
+    scores(stage, lane, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] *= qs;
+    const bool partial = lo > 0 || hi < kWarpTok;
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+        if (row < lo || row >= hi) s[i] = __int_as_float(0xff800000);
+      }
+    }
+    float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    mx -= kShift<FMT>;  // m carries the shift: weights are 2^(s - m)
+    const bool up = mx > m + kLazy;
+    if (__any_sync(0xffffffffu, up)) {
+      const float f = up ? ex2(m - mx) : 1.f;
+      if (up) m = mx;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i][0] *= f, o[i][1] *= f, o[i][2] *= f, o[i][3] *= f;
+    }
+    const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = ex2(s[i] - ref);
+      l += w[i];
+    }
+    // weights as hi + lo in 16 bits: rows 0..7 and 8..15 of the A fragment
+    constexpr int PF = kBf ? STARKV_KV_BF16 : STARKV_KV_F16;
+    uint32_t ah[2], al[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ah[i] = kv_pack<PF>(w[2 * i], w[2 * i + 1]);
+      const float2 h = kv_unpack<PF>(ah[i]);
+      al[i] = kv_pack<PF>(w[2 * i] - h.x, w[2 * i + 1] - h.y);
+    }
+    const uint32_t vs = stage + R::kKeys;
+    if (!kInt8) {
+      const int mi = lane / 8, row = lane % 8 + 8 * (mi & 1);
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t f[4];
+        ldsm4t(f, vs + chunk_at<false, D>(row, 2 * n + (mi >> 1)));
+        mma16816<kBf>(o[2 * n], ah[0], al[0], ah[1], al[1], f[0], f[1]);
+        mma16816<kBf>(o[2 * n + 1], ah[0], al[0], ah[1], al[1], f[2], f[3]);
+      }
+    } else {
+      // Column n = lane / 4 of product (jj, i) is channel 8 (n + 8 jj) + i: a lane decodes eight
+      // neighbouring channels of four tokens, code times scale rounded once to fp16.
+      const int g = lane / 4;
+      const uint32_t sc = stage + 2 * R::kKeys + R::kScales;
+#pragma unroll
+      for (int jj = 0; jj < D / 64; ++jj) {
+        const int u = g + 8 * jj;
+        uint32_t b[2][8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r0 = 2 * t + 8 * half;
+          uint2 x = ld_shared_v2(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
+          uint2 y = ld_shared_v2(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
+          uint32_t f2 = ld_shared_u16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
+                        (uint32_t)ld_shared_u16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
+          if (partial) {  // whatever the scales of rows that do not count hold
+            if (r0 < lo || r0 >= hi) f2 &= 0xffff0000u;
+            if (r0 + 1 < lo || r0 + 1 >= hi) f2 &= 0x0000ffffu;
+          }
+          const __half2 f = *reinterpret_cast<const __half2*>(&f2);
+#pragma unroll
+          for (int w2 = 0; w2 < 2; ++w2) {
+            const uint32_t xa = (w2 ? x.y : x.x) ^ 0x80808080u, ya = (w2 ? y.y : y.x) ^ 0x80808080u;
+            const uint32_t z[2] = {__byte_perm(xa, ya, 0x5140), __byte_perm(xa, ya, 0x7362)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t c = less1152(__byte_perm(z[i / 2], 0x64646464u, i % 2 ? 0x4342 : 0x4140));
+              const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
+              b[half][4 * w2 + i] = *reinterpret_cast<const uint32_t*>(&r);
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          mma16816<false>(o[8 * jj + i], ah[0], al[0], ah[1], al[1], b[0][i], b[1][i]);
+      }
+    }
+  }
+
+  // This warp's sums to shared memory: [row][D] and (m, l) per row.
+  __device__ __forceinline__ void put(float* os, float2* ml, int lane) {
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const int g = lane / 4, t = lane % 4;
+    if (t == 0) ml[g] = make_float2(m, l);
+    float* d = os + g * D;
+    if (!kInt8) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(d + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+    } else {
+#pragma unroll
+      for (int jj = 0; jj < D / 64; ++jj)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[8 * (2 * t + 8 * jj) + i] = o[8 * jj + i][0] + o[8 * jj + i][2];
+          d[8 * (2 * t + 1 + 8 * jj) + i] = o[8 * jj + i][1] + o[8 * jj + i][3];
+        }
+    }
+  }
+};
+
+template <int FMT>
+__device__ __forceinline__ uint16_t to16(float x) {
+  return static_cast<uint16_t>(kv_pack<FMT>(x, 0.f));
+}
+
+// Weight of a part with reference m under the common reference M (-inf: nothing there).
+__device__ __forceinline__ float part_weight(float m, float M) {
+  return m == __int_as_float(0xff800000) ? 0.f : ex2(m - M);
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(32 * kKvWarps, 2) kv_split_kernel(const KvDecodeParams p) {
+  using R = Ring<FMT, D>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t ring = smem_u32(smem) + warp * R::kBytes;
+  float* os = reinterpret_cast<float*>(smem + kKvWarps * R::kBytes);
+  float2* ml = reinterpret_cast<float2*>(os + kKvWarps * kKvRows * D);
+  const int heads = p.pool.Hkv * p.groups, G = p.pool.H / p.pool.Hkv;
+
+  pdl_wait();
+  pdl_launch_dependents();
+  long long before;
+  const long long total = sum_pages(p, lane, 0, before) * heads;
+  const long long parts = min((long long)gridDim.x, total);  // no CTA without a unit has a record
+  if (blockIdx.x >= parts) return;
+  const long long u0 = total * blockIdx.x / parts, u1 = total * (blockIdx.x + 1) / parts;
+  Cursor c = find(p, lane, heads, u0);  // consumer: start of the current segment
+  Cursor lead = c;                      // producer
+  long long to_load = u1 - u0, to_do = u1 - u0;
+  int rows[R::kStages];  // [lo, hi) of the tiles in the ring, oldest first
+#pragma unroll
+  for (int i = 0; i < R::kStages; ++i) rows[i] = 0;
+  int wr = 0, rd = 0;
+  auto issue = [&]() -> int {
+    int r = 0;
+    if (to_load > 0) {
+      const Tile t = tile_of(p, lead, warp);
+      if (t.lo < t.hi) {
+        load_tile<FMT, D>(p, t, ring + wr * R::kStage, warp, lane);
+        r = t.lo | t.hi << 8;
+      }
+      --to_load;
+      if (to_load > 0) lead.next(p, heads);
+    }
+    cp_commit();
+    wr = wr + 1 == R::kStages ? 0 : wr + 1;
+    return r;
+  };
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) rows[i] = issue();
+
+  Sums<FMT, D> sums;
+  while (to_do > 0) {
+    const int n = static_cast<int>(min((long long)(c.s.count - c.pg), to_do));
+    sums.begin(p, c.b, c.hv, lane);
+    for (int i = 0; i < n; ++i) {
+      rows[R::kStages - 1] = issue();
+      cp_wait<R::kStages - 1>();
+      __syncwarp();
+      const int lo = rows[0] & 255, hi = rows[0] >> 8;
+      if (lo < hi) sums.add(ring + rd * R::kStage, lo, hi, lane);
+      __syncwarp();  // the stage is free for the next issue
+      rd = rd + 1 == R::kStages ? 0 : rd + 1;
+#pragma unroll
+      for (int k = 0; k + 1 < R::kStages; ++k) rows[k] = rows[k + 1];
+    }
+    // join the four warps
+    sums.put(os + warp * kKvRows * D, ml + warp * kKvRows, lane);
+    __syncthreads();
+    const int g = c.hv / p.groups, r0 = c.hv % p.groups * kKvRows, nr = min(G - r0, kKvRows);
+    const bool whole = n == c.s.count;
+    const long long slot = (long long)blockIdx.x * 2 + (c.pg == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < nr * D; i += 32 * kKvWarps) {
+      const int r = i / D, ch = i % D;
+      float M = __int_as_float(0xff800000);
+#pragma unroll
+      for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, ml[w * kKvRows + r].x);
+      float acc = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kKvWarps; ++w) {
+        const float f = part_weight(ml[w * kKvRows + r].x, M);
+        l = fmaf(f, ml[w * kKvRows + r].y, l);
+        acc = fmaf(f, os[(w * kKvRows + r) * D + ch], acc);
+      }
+      if (whole) {
+        const long long row = (long long)c.b * p.pool.H + g * G + r0 + r;
+        p.out[row * D + ch] = to16<FMT>(M == __int_as_float(0xff800000) ? 0.f : acc / l);
+        if (p.lse && ch == 0) p.lse[row] = kLn2 * (M + log2f(l));
+      } else {
+        p.rec[(slot * kKvRows + r) * D + ch] = acc;
+        if (ch == 0) p.rec_ml[slot * kKvRows + r] = make_float2(M, l);
+      }
+    }
+    __syncthreads();
+    to_do -= n;
+    if (to_do > 0) c.next_segment(p, heads);
+  }
+}
+
+// Joins the records of the sequences that several CTAs shared; writes zeros for empty ones.  One
+// CTA per (query head, sequence), a thread per channel.
+template <int FMT, int D>
+__global__ void __launch_bounds__(D) kv_join_kernel(const KvDecodeParams p) {
+  __shared__ float w[kKvMaxCtas];
+  __shared__ float red[2];
+  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x % 32;
+  const int G = p.pool.H / p.pool.Hkv, heads = p.pool.Hkv * p.groups;
+  const int g = h / G, hv = g * p.groups + h % G / kKvRows, r = h % G % kKvRows;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long row = (long long)b * p.pool.H + h;
+  const int count = span_of(p, b).count;
+  if (threadIdx.x == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
+    atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+  if (count == 0) {
+    p.out[row * D + threadIdx.x] = 0;
+    if (p.lse && threadIdx.x == 0) p.lse[row] = __int_as_float(0xff800000);
+    return;
+  }
+  long long before;
+  const long long total = sum_pages(p, lane, b, before) * heads;
+  const long long s0 = before * heads + (long long)hv * count, s1 = s0 + count;
+  // CTA i of N = min(grid, T) holds the units [T i / N, T (i + 1) / N): unit u lies in CTA
+  // ((u + 1) N - 1) / T
+  const long long parts = min((long long)p.grid, total);
+  const int c0 = static_cast<int>(((s0 + 1) * parts - 1) / total), c1 = static_cast<int>((s1 * parts - 1) / total);
+  if (c0 == c1) return;
+  auto at = [&](int i) { return ((long long)i * 2 + (i == c0 ? 1 : 0)) * kKvRows + r; };
+  if (threadIdx.x < 32) {
+    float M = __int_as_float(0xff800000);
+    for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.rec_ml[at(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float l = 0.f;
+    for (int i = c0 + lane; i <= c1; i += 32) {
+      const float2 x = p.rec_ml[at(i)];
+      const float f = part_weight(x.x, M);
+      w[i - c0] = f;
+      l = fmaf(f, x.y, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[0] = M, red[1] = l;
+  }
+  __syncthreads();
+  float acc = 0.f;
+#pragma unroll 4
+  for (int i = c0; i <= c1; ++i) acc = fmaf(w[i - c0], p.rec[at(i) * D + threadIdx.x], acc);
+  const float M = red[0], l = red[1];
+  p.out[row * D + threadIdx.x] = to16<FMT>(M == __int_as_float(0xff800000) ? 0.f : acc / l);
+  if (p.lse && threadIdx.x == 0) p.lse[row] = kLn2 * (M + log2f(l));
+}
+
+template <int FMT, int D>
+cudaError_t decode_launch(const KvDecodeParams& p, cudaStream_t s) {
+  constexpr int smem = smem_bytes<FMT, D>();
+  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), smem, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_join_kernel<FMT, D>, dim3(p.pool.H, p.pool.batch), dim3(D), 0, s, p);
+}
+
+template <int FMT, int D>
+int ctas_per_sm() {
+  static_assert(smem_bytes<FMT, D>() <= 115712, "two CTAs per SM");
+  return 2;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_decode(const KvDecodeParams& p, cudaStream_t s) {
+  const int d = p.pool.d;
+  switch (p.pool.fmt) {
+    case STARKV_KV_BF16: return d == 64 ? decode_launch<STARKV_KV_BF16, 64>(p, s) : decode_launch<STARKV_KV_BF16, 128>(p, s);
+    case STARKV_KV_F16: return d == 64 ? decode_launch<STARKV_KV_F16, 64>(p, s) : decode_launch<STARKV_KV_F16, 128>(p, s);
+    case STARKV_KV_INT8: return d == 64 ? decode_launch<STARKV_KV_INT8, 64>(p, s) : decode_launch<STARKV_KV_INT8, 128>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int kv_decode_ctas_per_sm(int fmt, int d) {
+  switch (fmt) {
+    case STARKV_KV_BF16: return d == 64 ? ctas_per_sm<STARKV_KV_BF16, 64>() : ctas_per_sm<STARKV_KV_BF16, 128>();
+    case STARKV_KV_F16: return d == 64 ? ctas_per_sm<STARKV_KV_F16, 64>() : ctas_per_sm<STARKV_KV_F16, 128>();
+    default: return d == 64 ? ctas_per_sm<STARKV_KV_INT8, 64>() : ctas_per_sm<STARKV_KV_INT8, 128>();
+  }
+}
+
+}  // namespace starkv
