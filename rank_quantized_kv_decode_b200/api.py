@@ -73,8 +73,10 @@ def _check_decode(lay, q, block_table, seq_lens, Bk_t, Bv, out, status) -> None:
 
 
 def _stream(stream) -> int | None:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle: building torch's stream object costs 3 us a call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def make_config(n_q_heads: int, n_kv_heads: int, head_dim: int, d_model: int, key_rank: int,
@@ -330,51 +332,68 @@ def kv_rope_init(lay: L.KvLayout, max_pages: int, table: torch.Tensor, stream=No
             "starkv_kv_rope_init")
 
 
-def _check_kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int) -> None:
-    """[n_tok][heads][d]; a token's heads are contiguous, the tokens may be slices of wider rows."""
-    if t is None:
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.shape[0] < n_tok:
-        raise ValueError(f"{name}: expected shape ({n_tok}, {heads}, {d}), got {tuple(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
-
-
-def _kv_rows(t) -> tuple[int | None, int]:
-    """Pointer and token stride of such a tensor."""
-    if t is None:
-        return None, 0
-    if not t.is_cuda:
+# The checks below are those of _need and _ptr, ordered for a short way through: a decode step makes
+# several of these calls per layer and its kernels run for a few microseconds.
+def _kv_device(t) -> int:
+    """Device index of a call's cache, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    if t.device.index is not None and t.device.index != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"tensor on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return dev
 
 
-def _kv_pages(lay, cache) -> int:
-    return cache.numel() * cache.element_size() // lay.page_bytes
+def _kv_ptr(t, dev: int) -> int | None:
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("expected a CUDA tensor" if t.get_device() < 0 else
+                         f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _check_kv_batch(lay, q, block_table, seq_lens, status) -> int:
+def _kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int) -> int:
+    """Token stride of [n_tok][heads][d]; a token's heads are contiguous, the tokens may be slices of
+    wider rows."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < n_tok:
+        raise ValueError(f"{name}: expected shape ({n_tok}, {heads}, {d}), got {tuple(shape)}")
+    if strides[2] != 1 or (heads > 1 and strides[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {strides}")
+    return strides[0] if shape[0] > 1 else heads * d
+
+
+def _kv_row_ptr(t, dev: int) -> int:
+    if t.get_device() != dev:
+        return _kv_ptr(t, dev)  # raises
+    return t.data_ptr()
+
+
+def _check_kv_batch(lay, q, block_table, seq_lens, status) -> tuple[int, int]:
+    """(batch, row length of the block table)."""
     c = lay.cfg
     _need(seq_lens, "seq_lens", torch.int32, ndim=1)
     _need(block_table, "block_table", torch.int32, ndim=2)
-    batch = seq_lens.shape[0]
-    if block_table.shape[0] < batch:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows for {batch} sequences")
+    batch, (rows, width) = seq_lens.shape[0], block_table.shape
+    if rows < batch:
+        raise ValueError(f"block_table: {rows} rows for {batch} sequences")
     _need(q, "q", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim)
     _need(status, "status", torch.int32, 1)
-    return batch
+    return batch, width
 
 
 def _check_kv_sel(lay, sel, batch: int) -> int:
     _need(sel, "sel", torch.int32, ndim=3)
-    if sel.shape[0] < batch or sel.shape[1] != lay.cfg.n_kv_heads:
+    rows, heads, n_sel = sel.shape
+    if rows < batch or heads != lay.cfg.n_kv_heads:
         raise ValueError(f"sel: expected ({batch}, {lay.cfg.n_kv_heads}, pages), got {tuple(sel.shape)}")
-    return sel.shape[2]
+    return n_sel
 
 
 def kv_append(lay, k, v, tok_seq, tok_pos, block_table, cache, rope_table, status, q=None, q_out=None,
@@ -382,18 +401,19 @@ def kv_append(lay, k, v, tok_seq, tok_pos, block_table, cache, rope_table, statu
     """Rotate and store keys and values [n][H_kv][d] of new tokens (slices of a fused projection
     will do), update the bounds of the pages they complete, and rotate their queries into q_out."""
     c = lay.cfg
-    dt, n_tok = _KV_DTYPE[c.fmt], k.shape[0]
+    dt, n_tok, H, Hkv, d = _KV_DTYPE[c.fmt], k.shape[0], c.n_q_heads, c.n_kv_heads, c.head_dim
     _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
-    _need(q_out, "q_out", dt, n_tok * c.n_q_heads * c.head_dim)
-    _check_kv_rows(q, "q", dt, n_tok, c.n_q_heads, c.head_dim)
-    _check_kv_rows(k, "k", dt, n_tok, c.n_kv_heads, c.head_dim)
-    _check_kv_rows(v, "v", dt, n_tok, c.n_kv_heads, c.head_dim)
-    (qp, qs), (kp, ks), (vp, vs) = _kv_rows(q), _kv_rows(k), _kv_rows(v)
+    _need(q_out, "q_out", dt, n_tok * H * d)
+    qs = _kv_rows(q, "q", dt, n_tok, H, d) if q is not None else 0
+    ks, vs = _kv_rows(k, "k", dt, n_tok, Hkv, d), _kv_rows(v, "v", dt, n_tok, Hkv, d)
+    dev = _kv_device(cache)
+    rows, width = block_table.shape
     L.check(L.load().starkv_kv_append(
-        ctypes.byref(lay), qp, qs, kp, ks, vp, vs, n_tok, _ptr(tok_seq), _ptr(tok_pos),
-        _ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(rope_table),
-        rope_table.numel() * rope_table.element_size(), _ptr(cache), _kv_pages(lay, cache),
-        _ptr(q_out), _ptr(status), _stream(stream)), "starkv_kv_append")
+        ctypes.byref(lay), _kv_row_ptr(q, dev) if q is not None else None, qs, _kv_row_ptr(k, dev), ks,
+        _kv_row_ptr(v, dev), vs, n_tok, _kv_ptr(tok_seq, dev), _kv_ptr(tok_pos, dev),
+        _kv_ptr(block_table, dev), width, rows, _kv_ptr(rope_table, dev), rope_table.nbytes,
+        _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes, _kv_ptr(q_out, dev), _kv_ptr(status, dev),
+        _stream(stream)), "starkv_kv_append")
 
 
 def kv_gather(lay, cache, tok_seq, tok_pos, block_table, k_out, v_out, status, stream=None) -> None:
@@ -403,21 +423,24 @@ def kv_gather(lay, cache, tok_seq, tok_pos, block_table, k_out, v_out, status, s
     _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
     _need(k_out, "k_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
     _need(v_out, "v_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
+    dev = _kv_device(cache)
+    rows, width = block_table.shape
     L.check(L.load().starkv_kv_gather(
-        ctypes.byref(lay), _ptr(cache), _kv_pages(lay, cache), _ptr(tok_seq), _ptr(tok_pos), n_tok,
-        _ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(k_out), _ptr(v_out),
-        _ptr(status), _stream(stream)), "starkv_kv_gather")
+        ctypes.byref(lay), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes, _kv_ptr(tok_seq, dev),
+        _kv_ptr(tok_pos, dev), n_tok, _kv_ptr(block_table, dev), width, rows, _kv_ptr(k_out, dev),
+        _kv_ptr(v_out, dev), _kv_ptr(status, dev), _stream(stream)), "starkv_kv_gather")
 
 
 def kv_select(lay, q, cache, block_table, seq_lens, sel, status, keep_first: int = 0,
               keep_last: int = 1, stream=None) -> None:
     """Choose sel.shape[2] pages per sequence and KV head into sel [batch][H_kv][pages]."""
-    batch = _check_kv_batch(lay, q, block_table, seq_lens, status)
+    batch, width = _check_kv_batch(lay, q, block_table, seq_lens, status)
     n_sel = _check_kv_sel(lay, sel, batch)
+    dev = _kv_device(cache)
     L.check(L.load().starkv_kv_select(
-        ctypes.byref(lay), _ptr(q), _ptr(cache), _kv_pages(lay, cache), _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), batch, n_sel, keep_first, keep_last, _ptr(sel),
-        _ptr(status), _stream(stream)), "starkv_kv_select")
+        ctypes.byref(lay), _kv_ptr(q, dev), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes,
+        _kv_ptr(block_table, dev), width, _kv_ptr(seq_lens, dev), batch, n_sel, keep_first, keep_last,
+        _kv_ptr(sel, dev), _kv_ptr(status, dev), _stream(stream)), "starkv_kv_select")
 
 
 def kv_decode(lay, q, cache, block_table, seq_lens, out, workspace, status, sel=None, lse=None,
@@ -425,16 +448,20 @@ def kv_decode(lay, q, cache, block_table, seq_lens, out, workspace, status, sel=
     """Attention of one (rotated) token per sequence over its cached tokens, or over the pages of
     ``sel``."""
     c = lay.cfg
-    batch = _check_kv_batch(lay, q, block_table, seq_lens, status)
-    _need(out, "out", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim)
-    _need(lse, "lse", torch.float32, batch * c.n_q_heads)
+    batch, width = _check_kv_batch(lay, q, block_table, seq_lens, status)
+    rows = batch * c.n_q_heads
+    _need(out, "out", _KV_DTYPE[c.fmt], rows * c.head_dim)
+    _need(lse, "lse", torch.float32, rows)
     n_sel = _check_kv_sel(lay, sel, batch) if sel is not None else 0
-    opts = L.KvDecodeOpts(scale, window, max_ctas, 0)
+    opts = None
+    if scale or window or max_ctas:
+        opts = ctypes.byref(L.KvDecodeOpts(scale, window, max_ctas, 0))
+    dev = _kv_device(cache)
     L.check(L.load().starkv_kv_decode(
-        ctypes.byref(lay), _ptr(q), _ptr(cache), _kv_pages(lay, cache), _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), batch, _ptr(sel), n_sel, ctypes.byref(opts), _ptr(out),
-        _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-        _stream(stream)), "starkv_kv_decode")
+        ctypes.byref(lay), _kv_ptr(q, dev), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes,
+        _kv_ptr(block_table, dev), width, _kv_ptr(seq_lens, dev), batch, _kv_ptr(sel, dev), n_sel, opts,
+        _kv_ptr(out, dev), _kv_ptr(lse, dev), _kv_ptr(workspace, dev), workspace.nbytes,
+        _kv_ptr(status, dev), _stream(stream)), "starkv_kv_decode")
 
 
 def diag_bounded_wait(timeout_ms: int, status, stream=None) -> None:
