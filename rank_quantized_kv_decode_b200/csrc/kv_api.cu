@@ -174,6 +174,7 @@ starkv_status starkv_kv_append(const starkv_kv_layout* lay, const void* q, int64
   if (st != STARKV_OK) return st;
   if (n_tok < 0 || batch < 1) return fail(STARKV_ERR_INVALID_ARG, "n_tok < 0 or batch < 1");
   if (n_tok == 0) return STARKV_OK;
+  if (n_tok > (1 << 24)) return fail(STARKV_ERR_INVALID_ARG, "n_tok too large for one call; split the tokens");
   KvAppendParams p;
   std::memset(&p, 0, sizeof(p));
   st = fill_pool(lay, cache, num_pages, block_table, max_pages, batch, dev_status, p.pool);

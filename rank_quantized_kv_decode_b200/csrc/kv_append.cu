@@ -10,158 +10,303 @@
 namespace starkv {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = 8;
+constexpr int kRounds = 2;            // rounds of a warp's task, their loads in flight together
+constexpr int kFusedBoundsMax = 256;  // tokens up to which one launch does both (see launch below)
 
-// One CTA per token (and slice of its rows).  A row is one head of q, k or v; D/16 threads share
-// it, thread j with channels [8j, 8j+8) of each half: both members of a pair, 16-byte accesses,
-// and a scale group is four neighbouring threads.
+// A row is one head of q, k or v of a token; D/16 lanes share it, lane j with channels [8j, 8j+8) of
+// each half: both members of a pair, 16-byte accesses, and a scale group is four neighbouring lanes.
+template <int D>
+struct RowMap {
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes, kTask = kRows * kRounds;
+};
+
+struct Raw {
+  uint4 lo, hi;
+};
+template <int D>
+__device__ __forceinline__ Raw load_raw(const uint16_t* row, int j) {
+  return {*reinterpret_cast<const uint4*>(row + 8 * j), *reinterpret_cast<const uint4*>(row + D / 2 + 8 * j)};
+}
+
+// Cosines and sines of a position for the lane's eight pairs.
+template <int D>
+__device__ __forceinline__ void angles(const float2* rope, int pos, int j, float2 (&c)[8]) {
+  const float4* f = reinterpret_cast<const float4*>(rope + (pos % kTile) * (D / 2) + 8 * j);
+  const float4* g = reinterpret_cast<const float4*>(rope + (kTile + pos / kTile) * (D / 2) + 8 * j);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = f[i], y = g[i];
+    c[2 * i] = make_float2(x.x * y.x - x.y * y.y, x.x * y.y + x.y * y.x);
+    c[2 * i + 1] = make_float2(x.z * y.z - x.w * y.w, x.z * y.w + x.w * y.z);
+  }
+}
+
+template <int FMT>
+struct Row {
+  float lo[8], hi[8];
+  __device__ __forceinline__ void set(const Raw& r) {
+    const uint32_t l[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, h[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = kv_unpack<FMT>(l[i]), z = kv_unpack<FMT>(h[i]);
+      lo[2 * i] = a.x, lo[2 * i + 1] = a.y, hi[2 * i] = z.x, hi[2 * i + 1] = z.y;
+    }
+  }
+  __device__ __forceinline__ void rotate(const float2 (&c)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = lo[i], y = hi[i];
+      lo[i] = x * c[i].x - y * c[i].y;
+      hi[i] = y * c[i].x + x * c[i].y;
+    }
+  }
+  __device__ __forceinline__ Raw rounded() const {
+    uint32_t a[4], z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = kv_pack<FMT>(lo[2 * i], lo[2 * i + 1]), z[i] = kv_pack<FMT>(hi[2 * i], hi[2 * i + 1]);
+    return {make_uint4(a[0], a[1], a[2], a[3]), make_uint4(z[0], z[1], z[2], z[3])};
+  }
+  // Scales of the lane's two groups (whole warp).
+  __device__ __forceinline__ void scales(__half& sa, __half& sz) const {
+    float ma = 0.f, mz = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ma = fmaxf(ma, fabsf(lo[i])), mz = fmaxf(mz, fabsf(hi[i]));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
+    }
+    sa = store_dev::group_scale(ma, 127.f), sz = store_dev::group_scale(mz, 127.f);
+  }
+  // Codes under those scales: four bytes a word, lower half then upper half.
+  __device__ __forceinline__ void codes(float fa, float fz, uint32_t (&ca)[2], uint32_t (&cz)[2]) const {
+    ca[0] = ca[1] = cz[0] = cz[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ca[i / 4] |= (store_dev::quant_code(lo[i], fa, 127) & 255) << (8 * (i % 4));
+      cz[i / 4] |= (store_dev::quant_code(hi[i], fz, 127) & 255) << (8 * (i % 4));
+    }
+  }
+  __device__ __forceinline__ void from_codes(float fa, float fz, const uint2 a, const uint2 z) {
+    const uint32_t ca[2] = {a.x, a.y}, cz[2] = {z.x, z.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = fa * static_cast<float>(static_cast<int8_t>(ca[i / 4] >> (8 * (i % 4))));
+      hi[i] = fz * static_cast<float>(static_cast<int8_t>(cz[i / 4] >> (8 * (i % 4))));
+    }
+  }
+};
+
+__device__ __forceinline__ bool in_table(const KvPool& P, int b, int pos) {
+  return b >= 0 && b < P.batch && pos >= 0 && pos < P.max_pages * kPage;
+}
+
+// Bounds of one (page, KV head) by one warp, inside the append: `map` gives for each of the 64 slots the
+// token of this call that fills it (its key is made again from the input: another warp may still be
+// storing it) or -1 (the key is read from the page).  Four lanes a row, 32 channels of each half: D = 128
+// takes two warps, `side` 0 and 1.
 template <int FMT, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const KvAppendParams p) {
-  constexpr int TPR = D / 16, RPP = kAppendThreads / TPR, HALF = D / 2;
-  __shared__ float2 cs[HALF];
-  const int n = blockIdx.x, tid = threadIdx.x;
-  const int j = tid % TPR;
+__device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, int side, const short* map, int lane) {
+  const int j = 4 * side + lane % 4, r0 = lane / 4;
   const KvPool& P = p.pool;
+  const uint8_t* tile = page + P.off_heads + (long long)g * P.head_bytes;
+  const __half* sc = reinterpret_cast<const __half*>(tile + (FMT == STARKV_KV_INT8 ? P.off_ks : 0));
+  float mn[16], mx[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) mn[i] = __int_as_float(0x7f800000), mx[i] = __int_as_float(0xff800000);
+#pragma unroll
+  for (int r1 = 0; r1 < kPage; r1 += 8) {
+    const int r = r0 + r1, m = map[r];
+    Row<FMT> x;
+    if (FMT != STARKV_KV_INT8) {
+      const uint16_t* src = m < 0 ? reinterpret_cast<const uint16_t*>(tile) + r * D : p.k + m * p.k_stride + g * D;
+      x.set(load_raw<D>(src, j));
+      if (m >= 0) {
+        float2 c[8];
+        angles<D>(p.rope, p.tok_pos[m], j, c);
+        x.rotate(c);
+        x.set(x.rounded());
+      }
+    } else {
+      float2 c[8];
+      if (m >= 0) {
+        x.set(load_raw<D>(p.k + m * p.k_stride + g * D, j));
+        angles<D>(p.rope, p.tok_pos[m], j, c);
+        x.rotate(c);
+      } else {
+        const float fa = __half2float(sc[r * (D / 32) + j / 4]), fz = __half2float(sc[r * (D / 32) + D / 64 + j / 4]);
+        x.from_codes(fa, fz, *reinterpret_cast<const uint2*>(tile + r * D + 8 * j),
+                     *reinterpret_cast<const uint2*>(tile + r * D + D / 2 + 8 * j));
+      }
+      __half sa, sz;
+      x.scales(sa, sz);  // the whole warp shuffles
+      if (m >= 0) {
+        uint32_t ca[2], cz[2];
+        x.codes(__half2float(sa), __half2float(sz), ca, cz);
+        x.from_codes(__half2float(sa), __half2float(sz), make_uint2(ca[0], ca[1]), make_uint2(cz[0], cz[1]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mn[i] = fminf(mn[i], x.lo[i]), mx[i] = fmaxf(mx[i], x.lo[i]);
+      mn[8 + i] = fminf(mn[8 + i], x.hi[i]), mx[8 + i] = fmaxf(mx[8 + i], x.hi[i]);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      mn[i] = fminf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
+      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+    }
+  if (r0 == 0) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(page) + (long long)g * 2 * D + 8 * j;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // lower bounds of both halves, then upper
+      const float* v = (k < 2 ? mn : mx) + 8 * (k % 2);
+      *reinterpret_cast<uint4*>(dst + k * (D / 2)) =
+          make_uint4(kv_pack<FMT>(v[0], v[1]), kv_pack<FMT>(v[2], v[3]), kv_pack<FMT>(v[4], v[5]), kv_pack<FMT>(v[6], v[7]));
+    }
+  }
+}
+
+// One warp per task of kTask rows of a token (`slices` tasks a token); behind them, with BOUNDS, D / 64
+// warps per (token, KV head) that do something where the token completes its page.
+template <int FMT, int D, bool BOUNDS>
+__global__ void __launch_bounds__(32 * kAppendWarps, BOUNDS ? 2 : 4) kv_append_kernel(const KvAppendParams p, int slices) {
+  using R = RowMap<D>;
+  __shared__ short s_map[BOUNDS ? kAppendWarps : 1][kPage];
+  const KvPool& P = p.pool;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  long long task = (long long)blockIdx.x * kAppendWarps + warp;
+  const long long stores = (long long)p.n_tok * slices;
   pdl_wait();
   pdl_launch_dependents();
+  if (task >= stores) {
+    if (!BOUNDS) return;
+    task -= stores;
+    const int side = static_cast<int>(task % (D / 64));
+    task /= D / 64;
+    if (task >= (long long)p.n_tok * P.Hkv) return;
+    const int n = static_cast<int>(task / P.Hkv), g = static_cast<int>(task % P.Hkv);
+    const int b = p.tok_seq[n], pos = p.tok_pos[n];
+    if (!in_table(P, b, pos) || pos % kPage != kPage - 1) return;
+    uint8_t* page = kv_page(P, b, pos / kPage);
+    if (!page) return;
+    short* map = s_map[warp];
+    map[lane] = map[lane + 32] = -1;
+    __syncwarp();
+    for (int m = lane; m < p.n_tok; m += 32)
+      if (p.tok_seq[m] == b && p.tok_pos[m] >= 0 && p.tok_pos[m] / kPage == pos / kPage)
+        map[p.tok_pos[m] % kPage] = static_cast<short>(m);
+    __syncwarp();
+    bounds_in_call<FMT, D>(p, page, g, side, map, lane);
+    return;
+  }
+  const int n = static_cast<int>(task / slices), slice = static_cast<int>(task % slices);
+  const int j = lane % R::kLanes;
+  const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv, first = slice * R::kTask + lane / R::kLanes;
+  Raw raw[kRounds];
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int r = first + i * R::kRows;
+    raw[i].lo = raw[i].hi = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const uint16_t* src = r < nq             ? p.q + n * p.q_stride + r * D
+                            : r < nq + P.Hkv ? p.k + n * p.k_stride + (r - nq) * D
+                                             : p.v + n * p.v_stride + (r - nq - P.Hkv) * D;
+      raw[i] = load_raw<D>(src, j);
+    }
+  }
   const int b = p.tok_seq[n], pos = p.tok_pos[n];
   const bool pos_ok = pos >= 0 && pos < P.max_pages * kPage;
-  uint8_t* page = nullptr;
-  if (pos_ok && b >= 0 && b < P.batch) page = kv_page(P, b, pos / kPage);
-  if (!page && tid == 0 && blockIdx.y == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
-  if (tid < HALF && pos_ok) {
-    const float2 f = p.rope[(pos % kTile) * HALF + tid];
-    const float2 g = p.rope[(kTile + pos / kTile) * HALF + tid];
-    cs[tid] = make_float2(f.x * g.x - f.y * g.y, f.x * g.y + f.y * g.x);
-  }
-  __syncthreads();
+  uint8_t* page = in_table(P, b, pos) ? kv_page(P, b, pos / kPage) : nullptr;
+  if (!page && lane == 0 && slice == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
   const int slot = pos_ok ? pos % kPage : 0;
-  const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv;
   float2 c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = pos_ok ? cs[8 * j + i] : make_float2(0.f, 0.f);
-  // every thread of a warp makes the same number of rounds (the scale groups shuffle)
-  for (int r0 = blockIdx.y * RPP; r0 < rows; r0 += gridDim.y * RPP) {
-    const int r = r0 + tid / TPR;
+  for (int i = 0; i < 8; ++i) c[i] = make_float2(0.f, 0.f);
+  if (pos_ok) angles<D>(p.rope, pos, j, c);
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int r = first + i * R::kRows;
+    if (slice * R::kTask + i * R::kRows >= rows) break;  // the same for the whole warp
     const bool in = r < rows;
     const int kind = r < nq ? 0 : (r < nq + P.Hkv ? 1 : 2);
     const int h = kind == 0 ? r : (kind == 1 ? r - nq : r - nq - P.Hkv);
-    uint4 lo4 = make_uint4(0, 0, 0, 0), hi4 = lo4;
-    if (in) {
-      const uint16_t* src = kind == 0   ? p.q + n * p.q_stride
-                            : kind == 1 ? p.k + n * p.k_stride
-                                        : p.v + n * p.v_stride;
-      src += h * D + 8 * j;
-      lo4 = *reinterpret_cast<const uint4*>(src);
-      hi4 = *reinterpret_cast<const uint4*>(src + HALF);
-    }
-    float lo[8], hi[8];
-    const uint32_t lw[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hw[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = kv_unpack<FMT>(lw[i]), z = kv_unpack<FMT>(hw[i]);
-      lo[2 * i] = a.x, lo[2 * i + 1] = a.y, hi[2 * i] = z.x, hi[2 * i + 1] = z.y;
-    }
-    if (kind != 2) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = lo[i], y = hi[i];
-        lo[i] = x * c[i].x - y * c[i].y;
-        hi[i] = y * c[i].x + x * c[i].y;
-      }
-    }
-    uint16_t* dst16 = nullptr;
+    Row<FMT> x;
+    x.set(raw[i]);
+    if (kind != 2) x.rotate(c);
+    uint8_t* tile = page + P.off_heads + (long long)h * P.head_bytes + (kind == 2 ? P.off_v : 0);
+    uint16_t* dst = nullptr;
     if (kind == 0)
-      dst16 = p.q_out + ((long long)n * P.H + h) * D;
+      dst = p.q_out + ((long long)n * P.H + h) * D;
     else if (FMT != STARKV_KV_INT8 && page)
-      dst16 = reinterpret_cast<uint16_t*>(page + P.off_heads + (long long)h * P.head_bytes +
-                                          (kind == 2 ? P.off_v : 0)) + slot * D;
-    if (in && dst16) {
-      uint32_t a[4], z[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = kv_pack<FMT>(lo[2 * i], lo[2 * i + 1]);
-        z[i] = kv_pack<FMT>(hi[2 * i], hi[2 * i + 1]);
-      }
-      *reinterpret_cast<uint4*>(dst16 + 8 * j) = make_uint4(a[0], a[1], a[2], a[3]);
-      *reinterpret_cast<uint4*>(dst16 + HALF + 8 * j) = make_uint4(z[0], z[1], z[2], z[3]);
+      dst = reinterpret_cast<uint16_t*>(tile) + slot * D;
+    if (in && dst) {
+      const Raw o = x.rounded();
+      *reinterpret_cast<uint4*>(dst + 8 * j) = o.lo;
+      *reinterpret_cast<uint4*>(dst + D / 2 + 8 * j) = o.hi;
     }
-    if (FMT == STARKV_KV_INT8) {
-      float ma = 0.f, mz = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ma = fmaxf(ma, fabsf(lo[i])), mz = fmaxf(mz, fabsf(hi[i]));
-#pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-        mz = fmaxf(mz, __shfl_xor_sync(0xffffffffu, mz, o));
-      }
+    if (FMT == STARKV_KV_INT8 && slice * R::kTask + (i + 1) * R::kRows > nq) {  // not a round of queries alone
+      __half sa, sz;
+      x.scales(sa, sz);  // the whole warp shuffles
       if (in && kind != 0 && page) {
-        const __half sa = store_dev::group_scale(ma, 127.f), sz = store_dev::group_scale(mz, 127.f);
-        const float fa = __half2float(sa), fz = __half2float(sz);
-        uint8_t* tile = page + P.off_heads + (long long)h * P.head_bytes;
-        uint8_t* code = tile + (kind == 2 ? P.off_v : 0) + slot * D;
-        __half* sc = reinterpret_cast<__half*>(tile + (kind == 2 ? P.off_vs : P.off_ks)) + slot * (D / 32);
-        uint32_t ca[2] = {0, 0}, cz[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ca[i / 4] |= (store_dev::quant_code(lo[i], fa, 127) & 255) << (8 * (i % 4));
-          cz[i / 4] |= (store_dev::quant_code(hi[i], fz, 127) & 255) << (8 * (i % 4));
-        }
-        *reinterpret_cast<uint2*>(code + 8 * j) = make_uint2(ca[0], ca[1]);
-        *reinterpret_cast<uint2*>(code + HALF + 8 * j) = make_uint2(cz[0], cz[1]);
+        uint32_t ca[2], cz[2];
+        x.codes(__half2float(sa), __half2float(sz), ca, cz);
+        *reinterpret_cast<uint2*>(tile + slot * D + 8 * j) = make_uint2(ca[0], ca[1]);
+        *reinterpret_cast<uint2*>(tile + slot * D + D / 2 + 8 * j) = make_uint2(cz[0], cz[1]);
         if (j % 4 == 0) {
+          __half* sc = reinterpret_cast<__half*>(page + P.off_heads + (long long)h * P.head_bytes +
+                                                 (kind == 2 ? P.off_vs : P.off_ks)) + slot * (D / 32);
           sc[j / 4] = sa;
-          sc[HALF / 32 + j / 4] = sz;
+          sc[D / 64 + j / 4] = sz;
         }
       }
     }
   }
 }
 
-// Bounds of the pages that an append completed: per channel the smallest and largest stored key.
-// Runs after the append (its 64 keys may come from several CTAs and calls).  A CTA looks at
-// `span` tokens for those in slot 63; one warp reads one (page, KV head): 16-byte loads, a lane
-// keeps the same channels in every row.
-constexpr int kBoundsWarps = 8;
+// Bounds of the pages that an append of many tokens completed, after it: all keys are in the pages.  A
+// CTA looks at 64 tokens for those in slot 63 (one in 64 of a prompt's) and reads one KV head of their
+// pages, eight rows a warp.
 template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kBoundsWarps) kv_bounds_kernel(const KvAppendParams p, int span) {
+__global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p) {
   constexpr int CH = FMT == STARKV_KV_INT8 ? 16 : 8;  // channels of a 16-byte load
-  constexpr int CPR = D / CH, RPW = 32 / CPR;         // loads per row, rows per warp and round
-  __shared__ int hit[64];
+  constexpr int CPR = D / CH, RPW = 32 / CPR;         // loads per row, rows per warp and load
+  __shared__ int hit[kPage];
   __shared__ int hits;
+  __shared__ float s_mn[8][D], s_mx[8][D];
   const KvPool& P = p.pool;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0) hits = 0;
   __syncthreads();
-  if ((int)threadIdx.x < span) {
-    const int n = blockIdx.x * span + threadIdx.x;
-    if (n < p.n_tok) {
-      const int b = p.tok_seq[n], pos = p.tok_pos[n];
-      if (b >= 0 && b < P.batch && pos >= 0 && pos < P.max_pages * kPage && pos % kPage == kPage - 1)
-        hit[atomicAdd(&hits, 1)] = n;
-    }
+  if (threadIdx.x < kPage) {
+    const int n = blockIdx.x * kPage + threadIdx.x;
+    if (n < p.n_tok && in_table(P, p.tok_seq[n], p.tok_pos[n]) && p.tok_pos[n] % kPage == kPage - 1)
+      hit[atomicAdd(&hits, 1)] = n;
   }
   __syncthreads();
-  const int items = hits * P.Hkv;
-  for (int it = blockIdx.y * kBoundsWarps + warp; it < items; it += gridDim.y * kBoundsWarps) {
-    const int n = hit[it / P.Hkv], g = it % P.Hkv;
+  for (int it = 0; it < hits; ++it) {
+    const int n = hit[it];
     uint8_t* page = kv_page(P, p.tok_seq[n], p.tok_pos[n] / kPage);
-    if (!page) continue;
+    if (!page) continue;  // the same for the whole CTA
     const uint8_t* tile = page + P.off_heads + (long long)g * P.head_bytes;
-    const int ck = lane % CPR, r0 = lane / CPR;
+    const int ck = lane % CPR, r0 = 8 * warp + lane / CPR;
     float lo[CH], hi[CH];
 #pragma unroll
     for (int i = 0; i < CH; ++i) lo[i] = __int_as_float(0x7f800000), hi[i] = __int_as_float(0xff800000);
     const uint4* src = reinterpret_cast<const uint4*>(tile);
     const __half* sc = reinterpret_cast<const __half*>(tile + (FMT == STARKV_KV_INT8 ? P.off_ks : 0));
-#pragma unroll 8
-    for (int r = r0; r < kPage; r += RPW) {
-      const uint4 x = src[r * CPR + ck];
+#pragma unroll
+    for (int r = 0; r < 8; r += RPW) {
+      const uint4 x = src[(r0 + r) * CPR + ck];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
       if (FMT == STARKV_KV_INT8) {
-        const float s = __half2float(sc[r * (D / 32) + ck / 2]);
+        const float s = __half2float(sc[(r0 + r) * (D / 32) + ck / 2]);
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
           const float v = s * static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4))));
@@ -183,14 +328,22 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) kv_bounds_kernel(const KvAp
         lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
         hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
       }
-    if (r0 == 0) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(page + (long long)g * 2 * D * 2) + ck * (CH / 2);
+    if (lane < CPR)
 #pragma unroll
-      for (int i = 0; i < CH / 2; ++i) {
-        dst[i] = kv_pack<FMT>(lo[2 * i], lo[2 * i + 1]);
-        dst[D / 2 + i] = kv_pack<FMT>(hi[2 * i], hi[2 * i + 1]);
+      for (int i = 0; i < CH; ++i) s_mn[warp][ck * CH + i] = lo[i], s_mx[warp][ck * CH + i] = hi[i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      const int c = threadIdx.x % (D / 2) * 2;  // a pair of channels; the lower bounds, then the upper
+      const bool up = threadIdx.x >= D / 2;
+      float a = up ? s_mx[0][c] : s_mn[0][c], z = up ? s_mx[0][c + 1] : s_mn[0][c + 1];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) {
+        a = up ? fmaxf(a, s_mx[w][c]) : fminf(a, s_mn[w][c]);
+        z = up ? fmaxf(z, s_mx[w][c + 1]) : fminf(z, s_mn[w][c + 1]);
       }
+      reinterpret_cast<uint32_t*>(page + (long long)g * 4 * D)[threadIdx.x] = kv_pack<FMT>(a, z);
     }
+    __syncthreads();
   }
 }
 
@@ -238,16 +391,17 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) 
 
 template <int FMT, int D>
 cudaError_t append_launch(const KvAppendParams& p, cudaStream_t s) {
-  const int rpp = kAppendThreads / (D / 16);
   const int rows = (p.q ? p.pool.H : 0) + 2 * p.pool.Hkv;
-  // few tokens: one CTA per slice of the rows; many: a token's rows in one CTA
-  const int slices = p.n_tok < 512 ? (rows + rpp - 1) / rpp : 1;
-  cudaError_t e = launch_pdl(kv_append_kernel<FMT, D>, dim3(p.n_tok, slices), dim3(kAppendThreads), 0, s, p);
+  const int slices = (rows + RowMap<D>::kTask - 1) / RowMap<D>::kTask;
+  // Few tokens (decode steps, short prompts): the bounds in the same launch, where a completed page's
+  // warp looks through the call's tokens.  Many: a launch behind it.
+  const bool fused = p.n_tok <= kFusedBoundsMax;
+  const long long tasks = (long long)p.n_tok * (slices + (fused ? p.pool.Hkv * (D / 64) : 0));
+  const dim3 grid(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)), block(32 * kAppendWarps);
+  if (fused) return launch_pdl(kv_append_kernel<FMT, D, true>, grid, block, 0, s, p, slices);
+  const cudaError_t e = launch_pdl(kv_append_kernel<FMT, D, false>, grid, block, 0, s, p, slices);
   if (e != cudaSuccess) return e;
-  // few tokens: most may sit in slot 63 at once; many: one in 64 of a prompt does
-  const int span = p.n_tok <= 1024 ? 8 : 64;
-  return launch_pdl(kv_bounds_kernel<FMT, D>, dim3((p.n_tok + span - 1) / span, span == 8 ? p.pool.Hkv : 1),
-                    dim3(32 * kBoundsWarps), 0, s, p, span);
+  return launch_pdl(kv_bounds_kernel<FMT, D>, dim3((p.n_tok + kPage - 1) / kPage, p.pool.Hkv), dim3(256), 0, s, p);
 }
 
 }  // namespace

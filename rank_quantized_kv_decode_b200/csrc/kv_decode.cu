@@ -23,7 +23,6 @@
 namespace starkv {
 namespace {
 
-constexpr int kWarpTok = kPage / kKvWarps;  // 16: tokens of a warp's tile
 constexpr float kLazy = 8.f;  // the reference follows the running maximum when that is 2^8 above it:
                               // weights stay below 2^8, and O is rescaled a few times per sequence
 constexpr float kLn2 = 0.69314718055994531f;
@@ -56,6 +55,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// fp16, upper rows only, onto zero.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
+      "{%9,%9,%9,%9};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -84,12 +92,17 @@ __device__ __forceinline__ void cp_wait() {
 template <int FMT, int D>
 struct Ring {
   static constexpr bool kInt8 = FMT == STARKV_KV_INT8;
+  // Tokens of a warp's tile: 16, so that the four warps share every page; int8, whose time is
+  // instructions, 32, so that the steps of a tile that are not per token count half as much.
+  static constexpr int kTok = kInt8 ? 32 : 16;
+  static constexpr int kParts = kPage / kTok;          // warps that share a page
+  static constexpr int kPages = kKvWarps / kParts;     // pages that the CTA's warps take at a time
   static constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a token's keys (or values)
-  static constexpr int kKeys = kWarpTok * kRow;             // one tile's keys
-  static constexpr int kScales = kInt8 ? kWarpTok * (D / 32) * 2 : 0;
+  static constexpr int kKeys = kTok * kRow;                 // one tile's keys
+  static constexpr int kScales = kInt8 ? kTok * (D / 32) * 2 : 0;
   static constexpr int kStage = 2 * kKeys + 2 * kScales;
-  // two CTAs per SM (8 warps): about 96 KB of ring per CTA
-  static constexpr int kStages = (kInt8 ? (D == 128 ? 5 : 10) : (D == 128 ? 3 : 6));
+  static constexpr int kCtas = 2;  // per SM
+  static constexpr int kStages = kInt8 ? (D == 128 ? 2 : 5) : (D == 128 ? 3 : 6);
   static constexpr int kBytes = kStage * kStages;
 };
 template <int FMT, int D>
@@ -138,6 +151,12 @@ __device__ __forceinline__ long long sum_pages(const KvDecodeParams& p, int lane
   return all;
 }
 
+// x / y of non-negative numbers, by the short division where both fit.
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // A place in the list: sequence, KV head (and group of its query heads), page of the span.
 struct Cursor {
   int b, hv, pg;
@@ -152,8 +171,30 @@ struct Cursor {
       s = span_of(p, b);
     } while (s.count == 0);
   }
-  __device__ __forceinline__ void next(const KvDecodeParams& p, int heads) {
-    if (++pg == s.count) next_segment(p, heads);
+};
+
+// A warp's tiles of a CTA's share: pages phase, phase + STEP, ... of every segment.
+template <int STEP>
+struct Walk {
+  Cursor c;        // the segment's first page
+  int n, i;        // pages of the segment, the warp's place among them
+  long long left;  // pages of the share from this segment on; 0: done
+  __device__ __forceinline__ void begin(const Cursor& at, long long share, int phase, const KvDecodeParams& p, int heads) {
+    c = at, left = share;
+    n = static_cast<int>(min((long long)(c.s.count - c.pg), left)), i = phase;
+    settle(phase, p, heads);
+  }
+  __device__ __forceinline__ void next(int phase, const KvDecodeParams& p, int heads) {
+    i += STEP;
+    settle(phase, p, heads);
+  }
+  __device__ __forceinline__ void settle(int phase, const KvDecodeParams& p, int heads) {
+    while (i >= n) {
+      left -= n;
+      if (left == 0) return;
+      c.next_segment(p, heads);
+      n = static_cast<int>(min((long long)c.s.count, left)), i = phase;
+    }
   }
 };
 
@@ -177,8 +218,8 @@ __device__ __forceinline__ Cursor find(const KvDecodeParams& p, int lane, int he
       const long long start = (before + __shfl_sync(0xffffffffu, inc - n, l)) * heads;
       c.s = span_of(p, c.b);
       const long long in = u - start;
-      c.hv = static_cast<int>(in / max(c.s.count, 1));
-      c.pg = static_cast<int>(in % max(c.s.count, 1));
+      c.hv = static_cast<int>(quotient(in, max(c.s.count, 1)));
+      c.pg = static_cast<int>(in - (long long)c.hv * c.s.count);
       return c;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
@@ -191,12 +232,13 @@ struct Tile {
   const uint8_t* src;  // the head's tile of the page, or null
   int lo, hi;
 };
-__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Cursor& c, int warp) {
+template <int TOK>
+__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Cursor& c, int pg, int part) {
   Tile t{nullptr, 0, 0};
   const int g = c.hv / p.groups;
-  int i = c.s.first + c.pg;
+  int i = c.s.first + pg;
   if (p.sel) {
-    i = p.sel[((long long)c.b * p.pool.Hkv + g) * p.n_sel + c.pg];
+    i = p.sel[((long long)c.b * p.pool.Hkv + g) * p.n_sel + pg];
     if (i == -1) return t;
     if (i < 0 || i >= (c.s.len + kPage - 1) / kPage) {
       atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
@@ -209,17 +251,17 @@ __device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Cursor& c
     return t;
   }
   t.src = page + p.pool.off_heads + (long long)g * p.pool.head_bytes;
-  const int t0 = i * kPage + warp * kWarpTok;
-  t.hi = min(max(c.s.len - t0, 0), kWarpTok);
-  t.lo = p.window > 0 ? min(max(c.s.len - p.window - t0, 0), kWarpTok) : 0;
+  const int t0 = i * kPage + part * TOK;
+  t.hi = min(max(c.s.len - t0, 0), TOK);
+  t.lo = p.window > 0 ? min(max(c.s.len - p.window - t0, 0), TOK) : 0;
   return t;
 }
 
 template <int FMT, int D>
-__device__ __forceinline__ void load_tile(const KvDecodeParams& p, const Tile& t, uint32_t stage, int warp, int lane) {
+__device__ __forceinline__ void load_tile(const KvDecodeParams& p, const Tile& t, uint32_t stage, int part, int lane) {
   using R = Ring<FMT, D>;
-  constexpr int CPR = R::kRow / 16, N = kWarpTok * CPR;
-  const uint8_t* k = t.src + warp * R::kKeys;
+  constexpr int CPR = R::kRow / 16, N = R::kTok * CPR;
+  const uint8_t* k = t.src + part * R::kKeys;
   const uint8_t* v = k + p.pool.off_v;
 #pragma unroll
   for (int i = lane; i < N; i += 32) {
@@ -233,7 +275,7 @@ __device__ __forceinline__ void load_tile(const KvDecodeParams& p, const Tile& t
     if (lane < 2 * SC) {
       const int which = lane / SC, i = lane % SC;
       cp16(stage + 2 * R::kKeys + lane * 16,
-           t.src + (which ? p.pool.off_vs : p.pool.off_ks) + warp * R::kScales + i * 16, true);
+           t.src + (which ? p.pool.off_vs : p.pool.off_ks) + part * R::kScales + i * 16, true);
     }
   }
 }
@@ -243,6 +285,7 @@ template <int FMT, int D>
 struct Sums {
   static constexpr bool kInt8 = FMT == STARKV_KV_INT8;
   static constexpr bool kBf = FMT == STARKV_KV_BF16;
+  static constexpr int kTok = Ring<FMT, D>::kTok, kHalves = kTok / 8;  // 8-token columns of products
   uint32_t q[D / 16][2];  // A fragments of the queries: rows 0..7 (the lower half is zero)
   float qs;               // factor of the dot products: scale log2(e), int8: times the query's power of two
   float o[D / 8][4];      // O: [0,1] of the weights' high part, [2,3] of the low part
@@ -292,48 +335,50 @@ struct Sums {
     l = 0.f;
   }
 
-  // Scores (dot products) of the tile's tokens 2t, 2t+1, 8+2t, 9+2t for row lane / 4.
-  __device__ __forceinline__ void scores(uint32_t stage, int lane, float (&s)[4]) const {
+  // Scores (dot products) of the tile's tokens 8 h + 2t, 8 h + 2t + 1 for row lane / 4.
+  __device__ __forceinline__ void scores(uint32_t stage, int lane, float (&s)[2 * kHalves]) const {
     using R = Ring<FMT, D>;
-    if (!kInt8) {
-      float c[2][4] = {};
+    if constexpr (!kInt8) {
       const int mi = lane / 8, row = lane % 8 + 8 * (mi >> 1);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t f[4];
-        ldsm4(f, stage + chunk_at<false, D>(row, 2 * k + (mi & 1)));
-        mma16816<kBf>(c[0], q[k][0], 0u, q[k][1], 0u, f[0], f[1]);
-        mma16816<kBf>(c[1], q[k][0], 0u, q[k][1], 0u, f[2], f[3]);
+      for (int h = 0; h < kHalves; h += 2) {
+        float c[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t f[4];
+          ldsm4(f, stage + chunk_at<false, D>(8 * h + row, 2 * k + (mi & 1)));
+          mma16816<kBf>(c[0], q[k][0], 0u, q[k][1], 0u, f[0], f[1]);
+          mma16816<kBf>(c[1], q[k][0], 0u, q[k][1], 0u, f[2], f[3]);
+        }
+        s[2 * h] = c[0][0], s[2 * h + 1] = c[0][1], s[2 * h + 2] = c[1][0], s[2 * h + 3] = c[1][1];
       }
-      s[0] = c[0][0], s[1] = c[0][1], s[2] = c[1][0], s[3] = c[1][1];
     } else {
       const int g = lane / 4, t = lane % 4;
       const uint32_t sc = stage + 2 * R::kKeys;
-      s[0] = s[1] = s[2] = s[3] = 0.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int h = 0; h < kHalves; ++h) {
         // the fp32 scales of this lane's two result columns
         float f[2][D / 32];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            const uint32_t w = ld_shared_u32(sc + (8 * half + 2 * t + i) * (D / 16) + 4 * j);
+            const uint32_t w = ld_shared_u32(sc + (8 * h + 2 * t + i) * (D / 16) + 4 * j);
             const float2 x = kv_unpack<STARKV_KV_F16>(w);
             f[i][2 * j] = x.x, f[i][2 * j + 1] = x.y;
           }
-        const int row = g + 8 * half;
+        const int row = g + 8 * h;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           const uint2 w = ld_shared_v2(stage + chunk_at<true, D>(row, 2 * j) + 8 * t);
-          uint32_t h[4];
-          halves(w.x, h[0], h[1]);
-          halves(w.y, h[2], h[3]);
-          float c[4] = {};
-          mma16816<false>(c, q[2 * j][0], 0u, q[2 * j][1], 0u, h[0], h[1]);
-          mma16816<false>(c, q[2 * j + 1][0], 0u, q[2 * j + 1][1], 0u, h[2], h[3]);
-          s[2 * half] = fmaf(c[0], f[0][j], s[2 * half]);
-          s[2 * half + 1] = fmaf(c[1], f[1][j], s[2 * half + 1]);
+          uint32_t x[4];
+          halves(w.x, x[0], x[1]);
+          halves(w.y, x[2], x[3]);
+          float c[4];
+          mma16816_zero(c, q[2 * j][0], q[2 * j][1], x[0], x[1]);
+          mma16816<false>(c, q[2 * j + 1][0], 0u, q[2 * j + 1][1], 0u, x[2], x[3]);
+          s[2 * h] = j ? fmaf(c[0], f[0][j], s[2 * h]) : c[0] * f[0][j];
+          s[2 * h + 1] = j ? fmaf(c[1], f[1][j], s[2 * h + 1]) : c[1] * f[1][j];
         }
       }
     }
@@ -354,20 +399,23 @@ struct Sums {
   // Adds the tile's rows [lo, hi) of keys and values at `stage`.
   __device__ __forceinline__ void add(uint32_t stage, int lo, int hi, int lane) {
     using R = Ring<FMT, D>;
+    constexpr int N = 2 * kHalves;  // scores of a lane
     const int t = lane % 4;
-    float s[4];
+    float s[N];
     scores(stage, lane, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] *= qs;
-    const bool partial = lo > 0 || hi < kWarpTok;
+    for (int i = 0; i < N; ++i) s[i] *= qs;
+    const bool partial = lo > 0 || hi < kTok;
     if (partial) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N; ++i) {
         const int row = 2 * t + (i & 1) + 8 * (i >> 1);
         if (row < lo || row >= hi) s[i] = __int_as_float(0xff800000);
       }
     }
-    float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+    float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+    for (int i = 2; i < N; i += 2) mx = fmaxf(mx, fmaxf(s[i], s[i + 1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     mx -= kShift<FMT>;  // m carries the shift: weights are 2^(s - m)
@@ -380,68 +428,68 @@ struct Sums {
       for (int i = 0; i < D / 8; ++i) o[i][0] *= f, o[i][1] *= f, o[i][2] *= f, o[i][3] *= f;
     }
     const float ref = m == __int_as_float(0xff800000) ? 0.f : m;
-    float w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      w[i] = ex2(s[i] - ref);
-      l += w[i];
-    }
-    // weights as hi + lo in 16 bits: rows 0..7 and 8..15 of the A fragment
+    // weights as hi + lo in 16 bits: rows 0..7 and 8..15 of the A fragments
     constexpr int PF = kBf ? STARKV_KV_BF16 : STARKV_KV_F16;
-    uint32_t ah[2], al[2];
+    uint32_t ah[kHalves], al[kHalves];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ah[i] = kv_pack<PF>(w[2 * i], w[2 * i + 1]);
+    for (int i = 0; i < kHalves; ++i) {
+      const float w0 = ex2(s[2 * i] - ref), w1 = ex2(s[2 * i + 1] - ref);
+      l += w0 + w1;
+      ah[i] = kv_pack<PF>(w0, w1);
       const float2 h = kv_unpack<PF>(ah[i]);
-      al[i] = kv_pack<PF>(w[2 * i] - h.x, w[2 * i + 1] - h.y);
+      al[i] = kv_pack<PF>(w0 - h.x, w1 - h.y);
     }
     const uint32_t vs = stage + R::kKeys;
-    if (!kInt8) {
+    if constexpr (!kInt8) {
       const int mi = lane / 8, row = lane % 8 + 8 * (mi & 1);
 #pragma unroll
-      for (int n = 0; n < D / 16; ++n) {
-        uint32_t f[4];
-        ldsm4t(f, vs + chunk_at<false, D>(row, 2 * n + (mi >> 1)));
-        mma16816<kBf>(o[2 * n], ah[0], al[0], ah[1], al[1], f[0], f[1]);
-        mma16816<kBf>(o[2 * n + 1], ah[0], al[0], ah[1], al[1], f[2], f[3]);
-      }
+      for (int h = 0; h < kHalves; h += 2)
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t f[4];
+          ldsm4t(f, vs + chunk_at<false, D>(8 * h + row, 2 * n + (mi >> 1)));
+          mma16816<kBf>(o[2 * n], ah[h], al[h], ah[h + 1], al[h + 1], f[0], f[1]);
+          mma16816<kBf>(o[2 * n + 1], ah[h], al[h], ah[h + 1], al[h + 1], f[2], f[3]);
+        }
     } else {
       // Column n = lane / 4 of product (jj, i) is channel 8 (n + 8 jj) + i: a lane decodes eight
       // neighbouring channels of four tokens, code times scale rounded once to fp16.
       const int g = lane / 4;
       const uint32_t sc = stage + 2 * R::kKeys + R::kScales;
 #pragma unroll
-      for (int jj = 0; jj < D / 64; ++jj) {
-        const int u = g + 8 * jj;
-        uint32_t b[2][8];
+      for (int h = 0; h < kHalves; h += 2)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r0 = 2 * t + 8 * half;
-          uint2 x = ld_shared_v2(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
-          uint2 y = ld_shared_v2(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
-          uint32_t f2 = ld_shared_u16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
-                        (uint32_t)ld_shared_u16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
-          if (partial) {  // whatever the scales of rows that do not count hold
-            if (r0 < lo || r0 >= hi) f2 &= 0xffff0000u;
-            if (r0 + 1 < lo || r0 + 1 >= hi) f2 &= 0x0000ffffu;
-          }
-          const __half2 f = *reinterpret_cast<const __half2*>(&f2);
+        for (int jj = 0; jj < D / 64; ++jj) {
+          const int u = g + 8 * jj;
+          uint32_t b[2][8];
 #pragma unroll
-          for (int w2 = 0; w2 < 2; ++w2) {
-            const uint32_t xa = (w2 ? x.y : x.x) ^ 0x80808080u, ya = (w2 ? y.y : y.x) ^ 0x80808080u;
-            const uint32_t z[2] = {__byte_perm(xa, ya, 0x5140), __byte_perm(xa, ya, 0x7362)};
+          for (int e = 0; e < 2; ++e) {
+            const int r0 = 2 * t + 8 * (h + e);
+            const uint2 x = ld_shared_v2(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
+            const uint2 y = ld_shared_v2(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
+            uint32_t f2 = ld_shared_u16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
+                          (uint32_t)ld_shared_u16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
+            if (partial) {  // whatever the scales of rows that do not count hold
+              if (r0 < lo || r0 >= hi) f2 &= 0xffff0000u;
+              if (r0 + 1 < lo || r0 + 1 >= hi) f2 &= 0x0000ffffu;
+            }
+            const __half2 f = *reinterpret_cast<const __half2*>(&f2);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t c = less1152(__byte_perm(z[i / 2], 0x64646464u, i % 2 ? 0x4342 : 0x4140));
-              const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
-              b[half][4 * w2 + i] = *reinterpret_cast<const uint32_t*>(&r);
+            for (int w2 = 0; w2 < 2; ++w2) {
+              const uint32_t xa = (w2 ? x.y : x.x) ^ 0x80808080u, ya = (w2 ? y.y : y.x) ^ 0x80808080u;
+              const uint32_t z[2] = {__byte_perm(xa, ya, 0x5140), __byte_perm(xa, ya, 0x7362)};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t c = less1152(__byte_perm(z[i / 2], 0x64646464u, i % 2 ? 0x4342 : 0x4140));
+                const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&c), f);
+                b[e][4 * w2 + i] = *reinterpret_cast<const uint32_t*>(&r);
+              }
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          mma16816<false>(o[8 * jj + i], ah[0], al[0], ah[1], al[1], b[0][i], b[1][i]);
-      }
+          for (int i = 0; i < 8; ++i)
+            mma16816<false>(o[8 * jj + i], ah[h], al[h], ah[h + 1], al[h + 1], b[0][i], b[1][i]);
+        }
     }
   }
 
@@ -479,7 +527,7 @@ __device__ __forceinline__ float part_weight(float m, float M) {
 }
 
 template <int FMT, int D>
-__global__ void __launch_bounds__(32 * kKvWarps, 2) kv_split_kernel(const KvDecodeParams p) {
+__global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_kernel(const KvDecodeParams p) {
   using R = Ring<FMT, D>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -494,24 +542,25 @@ __global__ void __launch_bounds__(32 * kKvWarps, 2) kv_split_kernel(const KvDeco
   const long long total = sum_pages(p, lane, 0, before) * heads;
   const long long parts = min((long long)gridDim.x, total);  // no CTA without a unit has a record
   if (blockIdx.x >= parts) return;
-  const long long u0 = total * blockIdx.x / parts, u1 = total * (blockIdx.x + 1) / parts;
+  const long long u0 = quotient(total * blockIdx.x, parts), u1 = quotient(total * (blockIdx.x + 1), parts);
+  const int part = warp % R::kParts, phase = warp / R::kParts;
   Cursor c = find(p, lane, heads, u0);  // consumer: start of the current segment
-  Cursor lead = c;                      // producer
-  long long to_load = u1 - u0, to_do = u1 - u0;
+  Walk<R::kPages> lead;                 // producer
+  lead.begin(c, u1 - u0, phase, p, heads);
+  long long to_do = u1 - u0;
   int rows[R::kStages];  // [lo, hi) of the tiles in the ring, oldest first
 #pragma unroll
   for (int i = 0; i < R::kStages; ++i) rows[i] = 0;
   int wr = 0, rd = 0;
   auto issue = [&]() -> int {
     int r = 0;
-    if (to_load > 0) {
-      const Tile t = tile_of(p, lead, warp);
+    if (lead.left > 0) {
+      const Tile t = tile_of<R::kTok>(p, lead.c, lead.c.pg + lead.i, part);
       if (t.lo < t.hi) {
-        load_tile<FMT, D>(p, t, ring + wr * R::kStage, warp, lane);
+        load_tile<FMT, D>(p, t, ring + wr * R::kStage, part, lane);
         r = t.lo | t.hi << 8;
       }
-      --to_load;
-      if (to_load > 0) lead.next(p, heads);
+      lead.next(phase, p, heads);
     }
     cp_commit();
     wr = wr + 1 == R::kStages ? 0 : wr + 1;
@@ -524,7 +573,7 @@ __global__ void __launch_bounds__(32 * kKvWarps, 2) kv_split_kernel(const KvDeco
   while (to_do > 0) {
     const int n = static_cast<int>(min((long long)(c.s.count - c.pg), to_do));
     sums.begin(p, c.b, c.hv, lane);
-    for (int i = 0; i < n; ++i) {
+    for (int i = phase; i < n; i += R::kPages) {
       rows[R::kStages - 1] = issue();
       cp_wait<R::kStages - 1>();
       __syncwarp();
@@ -568,24 +617,25 @@ __global__ void __launch_bounds__(32 * kKvWarps, 2) kv_split_kernel(const KvDeco
   }
 }
 
-// Joins the records of the sequences that several CTAs shared; writes zeros for empty ones.  One
-// CTA per (query head, sequence), a thread per channel.
+// Joins the records of the sequences that several CTAs shared; writes zeros for empty ones.  One warp
+// per (sequence, query head), no shared memory, so that its CTAs can wait beside the split kernel's.  A
+// record is read by eight lanes (D / 8 channels each): four records a round, four rounds in flight.
 template <int FMT, int D>
-__global__ void __launch_bounds__(D) kv_join_kernel(const KvDecodeParams p) {
-  __shared__ float w[kKvMaxCtas];
-  __shared__ float red[2];
-  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x % 32;
+__global__ void __launch_bounds__(32) kv_join_kernel(const KvDecodeParams p) {
+  constexpr int N4 = D / 32;  // 16-byte loads of a lane's share of a record
+  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x, part = lane % 8, sub = lane / 8;
   const int G = p.pool.H / p.pool.Hkv, heads = p.pool.Hkv * p.groups;
   const int g = h / G, hv = g * p.groups + h % G / kKvRows, r = h % G % kKvRows;
   pdl_wait();
   pdl_launch_dependents();
   const long long row = (long long)b * p.pool.H + h;
   const int count = span_of(p, b).count;
-  if (threadIdx.x == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
+  if (lane == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
     atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+  uint2* out = reinterpret_cast<uint2*>(p.out + row * D);
   if (count == 0) {
-    p.out[row * D + threadIdx.x] = 0;
-    if (p.lse && threadIdx.x == 0) p.lse[row] = __int_as_float(0xff800000);
+    if (lane < D / 4) out[lane] = make_uint2(0, 0);
+    if (p.lse && lane == 0) p.lse[row] = __int_as_float(0xff800000);
     return;
   }
   long long before;
@@ -594,32 +644,41 @@ __global__ void __launch_bounds__(D) kv_join_kernel(const KvDecodeParams p) {
   // CTA i of N = min(grid, T) holds the units [T i / N, T (i + 1) / N): unit u lies in CTA
   // ((u + 1) N - 1) / T
   const long long parts = min((long long)p.grid, total);
-  const int c0 = static_cast<int>(((s0 + 1) * parts - 1) / total), c1 = static_cast<int>((s1 * parts - 1) / total);
+  const int c0 = static_cast<int>(quotient((s0 + 1) * parts - 1, total));
+  const int c1 = static_cast<int>(quotient(s1 * parts - 1, total));
   if (c0 == c1) return;
   auto at = [&](int i) { return ((long long)i * 2 + (i == c0 ? 1 : 0)) * kKvRows + r; };
-  if (threadIdx.x < 32) {
-    float M = __int_as_float(0xff800000);
-    for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.rec_ml[at(i)].x);
+  float M = __int_as_float(0xff800000);
+  for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.rec_ml[at(i)].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float l = 0.f;
-    for (int i = c0 + lane; i <= c1; i += 32) {
-      const float2 x = p.rec_ml[at(i)];
-      const float f = part_weight(x.x, M);
-      w[i - c0] = f;
-      l = fmaf(f, x.y, l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) red[0] = M, red[1] = l;
-  }
-  __syncthreads();
-  float acc = 0.f;
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float l = 0.f, acc[4 * N4] = {};
 #pragma unroll 4
-  for (int i = c0; i <= c1; ++i) acc = fmaf(w[i - c0], p.rec[at(i) * D + threadIdx.x], acc);
-  const float M = red[0], l = red[1];
-  p.out[row * D + threadIdx.x] = to16<FMT>(M == __int_as_float(0xff800000) ? 0.f : acc / l);
-  if (p.lse && threadIdx.x == 0) p.lse[row] = kLn2 * (M + log2f(l));
+  for (int i = c0 + sub; i <= c1; i += 4) {
+    const float2 x = p.rec_ml[at(i)];
+    const float f = part_weight(x.x, M);
+    l = fmaf(f, x.y, l);
+    const float4* rec = reinterpret_cast<const float4*>(p.rec + at(i) * D) + part;
+#pragma unroll
+    for (int k = 0; k < N4; ++k) {
+      const float4 v = rec[8 * k];
+      acc[4 * k] = fmaf(f, v.x, acc[4 * k]), acc[4 * k + 1] = fmaf(f, v.y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(f, v.z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(f, v.w, acc[4 * k + 3]);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+    for (int k = 0; k < 4 * N4; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+  }
+  const float inv = M == __int_as_float(0xff800000) ? 0.f : 1.f / l;
+#pragma unroll
+  for (int k = 0; k < N4; ++k)
+    if (sub == k % 4)
+      out[8 * k + part] = make_uint2(kv_pack<FMT>(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                                     kv_pack<FMT>(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+  if (p.lse && lane == 0) p.lse[row] = kLn2 * (M + log2f(l));
 }
 
 template <int FMT, int D>
@@ -629,13 +688,14 @@ cudaError_t decode_launch(const KvDecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), smem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_join_kernel<FMT, D>, dim3(p.pool.H, p.pool.batch), dim3(D), 0, s, p);
+  return launch_pdl(kv_join_kernel<FMT, D>, dim3(p.pool.H, p.pool.batch), dim3(32), 0, s, p);
 }
 
 template <int FMT, int D>
 int ctas_per_sm() {
-  static_assert(smem_bytes<FMT, D>() <= 115712, "two CTAs per SM");
-  return 2;
+  constexpr int n = Ring<FMT, D>::kCtas;
+  static_assert(n * (smem_bytes<FMT, D>() + 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
+  return n;
 }
 
 }  // namespace
