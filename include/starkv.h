@@ -459,13 +459,13 @@ typedef struct {
 typedef struct {
   size_t cache_bytes;            /* num_pages * page_bytes                                   */
   size_t rope_table_bytes;       /* table for positions < max_pages * 64                     */
-  size_t decode_workspace_bytes; /* partial records of one decode call, any batch and length */
+  size_t decode_workspace_bytes; /* partial records of a decode call of this batch, max_pages */
 } starkv_kv_sizes;
 
 /* Host only, pure. */
 STARKV_API starkv_status starkv_kv_layout_init(const starkv_kv_config* cfg, starkv_kv_layout* out);
 STARKV_API starkv_status starkv_kv_alloc(const starkv_kv_layout* lay, int64_t num_pages,
-                                         int32_t max_pages, starkv_kv_sizes* out);
+                                         int32_t batch, int32_t max_pages, starkv_kv_sizes* out);
 
 /* The table of starkv_rope_init for this layout's head_dim and rope_theta. */
 STARKV_API starkv_status starkv_kv_rope_init(const starkv_kv_layout* lay, int32_t max_pages,
@@ -541,13 +541,14 @@ typedef struct {
  *             with a window (INVALID_ARG)
  *   out       device [batch][H][d] in the type of q
  *   lse       device fp32 [batch][H]: ln sum_t exp(scale q_h . k_t), or NULL
- *   workspace device, >= decode_workspace_bytes; two calls that may overlap on the GPU need two
+ *   workspace device, >= decode_workspace_bytes for this call's batch and max_pages; two calls
+ *             that may overlap on the GPU need two.  It needs no initial values
  * An empty sequence gives zeros and -inf.  Tokens of a bad block-table entry are flagged and
  * skipped; a seq_len above max_pages * 64 is flagged and cut.  Rows of the last page behind the
  * sequence, and before the window, are never read into a sum, whatever they hold; an infinite
  * value that does count gives an infinity or a NaN in its channel.
- * Two launches: a split kernel, whose CTAs take equal shares of all pages of the batch, and a
- * join of the sequences that were split.  Results do not depend on timing. */
+ * Two launches: a split kernel, whose CTAs draw chunks of the batch's pages, and a join of the
+ * sequences that were split.  Results do not depend on timing. */
 STARKV_API starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q,
                                           const void* cache, int64_t num_pages,
                                           const int32_t* block_table, int32_t max_pages,

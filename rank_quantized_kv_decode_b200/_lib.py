@@ -112,7 +112,7 @@ EXPORTS = {
     "starkv_decode_combine_absorbed": (i32, [ctypes.POINTER(Layout), vp, i32, i32, vp, i32, vp, sz,
                                              vp, sz, vp, vp]),
     "starkv_kv_layout_init": (i32, [ctypes.POINTER(KvConfig), ctypes.POINTER(KvLayout)]),
-    "starkv_kv_alloc": (i32, [ctypes.POINTER(KvLayout), i64, i32, ctypes.POINTER(KvSizes)]),
+    "starkv_kv_alloc": (i32, [ctypes.POINTER(KvLayout), i64, i32, i32, ctypes.POINTER(KvSizes)]),
     "starkv_kv_rope_init": (i32, [ctypes.POINTER(KvLayout), i32, vp, sz, vp]),
     "starkv_kv_append": (i32, [ctypes.POINTER(KvLayout), vp, i64, vp, i64, vp, i64, i32, vp, vp, vp,
                                i32, i32, vp, sz, vp, i64, vp, vp, vp]),

@@ -319,9 +319,9 @@ def kv_layout_init(cfg: L.KvConfig) -> L.KvLayout:
     return lay
 
 
-def kv_alloc(lay: L.KvLayout, num_pages: int, max_pages: int) -> L.KvSizes:
+def kv_alloc(lay: L.KvLayout, num_pages: int, batch: int, max_pages: int) -> L.KvSizes:
     s = L.KvSizes()
-    L.check(L.load().starkv_kv_alloc(ctypes.byref(lay), num_pages, max_pages, ctypes.byref(s)),
+    L.check(L.load().starkv_kv_alloc(ctypes.byref(lay), num_pages, batch, max_pages, ctypes.byref(s)),
             "starkv_kv_alloc")
     return s
 
@@ -518,7 +518,7 @@ class KvCache:
     @classmethod
     def create(cls, lay: L.KvLayout, num_pages: int, batch: int, max_pages: int,
                device="cuda") -> "KvCache":
-        s = kv_alloc(lay, num_pages, max_pages)
+        s = kv_alloc(lay, num_pages, batch, max_pages)
         c = cls(lay, num_pages, batch, max_pages, _bytes(s.cache_bytes, device),
                 _bytes(s.rope_table_bytes, device), _bytes(s.decode_workspace_bytes, device),
                 torch.zeros(1, dtype=torch.int32, device=device))

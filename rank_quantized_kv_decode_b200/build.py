@@ -10,6 +10,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -33,16 +35,24 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         lib_t = os.path.getmtime(LIB)
         if all(os.path.getmtime(d) <= lib_t for d in deps):
             return LIB
-    cmd = [nvcc_path(), "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a",
-           "-lineinfo", "-Xcompiler", "-fPIC", "-shared", "-Xcompiler", "-fvisibility=hidden",
-           "-o", LIB + ".tmp", *srcs]
+    flags = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
+             "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
     if verbose_ptxas:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    proc = subprocess.run(cmd, cwd=CSRC, capture_output=True, text=True)
-    if proc.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + proc.stdout + proc.stderr)
+        flags = ["-Xptxas", "-v"] + flags
+
+    def run(args: list[str]) -> str:
+        proc = subprocess.run([nvcc_path(), *args], cwd=CSRC, capture_output=True, text=True)
+        if proc.returncode != 0:
+            raise RuntimeError("nvcc failed:\n" + proc.stdout + proc.stderr)
+        return proc.stdout + proc.stderr
+
+    # the sources side by side, then one link
+    with tempfile.TemporaryDirectory() as tmp, ThreadPoolExecutor(os.cpu_count()) as pool:
+        objs = [os.path.join(tmp, os.path.basename(s) + ".o") for s in srcs]
+        logs = list(pool.map(lambda so: run([*flags, "-c", "-o", so[1], so[0]]), zip(srcs, objs)))
+        run([*flags, "-shared", "-o", LIB + ".tmp", *objs])
     if verbose_ptxas:
-        sys.stderr.write(proc.stdout + proc.stderr)
+        sys.stderr.write("".join(logs))
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

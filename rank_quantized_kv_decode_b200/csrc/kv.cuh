@@ -5,8 +5,12 @@
 namespace starkv {
 
 constexpr int kKvRows = 8;         // query heads of one KV head that a CTA takes together
-constexpr int kKvMaxCtas = 512;    // most CTAs of the split kernel (two partial records each)
-constexpr int kKvWarps = 4;        // warps of a split CTA; each takes 16 of a page's 64 tokens
+constexpr int kKvMaxCtas = 296;    // most CTAs of the split kernel: two on each of 148 SMs
+constexpr int kKvRounds = 8;       // small chunks per warp that a list is cut into, at most
+constexpr int kKvWarps = 4;        // warps of a split CTA
+
+// Tokens of a tile, a warp's step (see the split kernel).
+constexpr int kv_tile_tokens(int fmt) { return fmt == STARKV_KV_INT8 ? 32 : 16; }
 
 // Where a token or page lies (offsets as in starkv_kv_layout).
 struct KvPool {
@@ -55,8 +59,10 @@ struct KvDecodeParams {
   float scale2;     // scale * log2(e)
   uint16_t* out;    // [batch][H][d]
   float* lse;       // [batch][H] or null
-  float* rec;       // [grid][2][kKvRows][d] partial sums
-  float2* rec_ml;   // [grid][2][kKvRows] reference (log2 units), sum
+  unsigned long long* counter;  // chunks drawn
+  float* rec;       // [piece][rec_rows][d] partial sums; piece = chunk + flat (sequence, KV head, group)
+  float2* rec_ml;   // [piece][rec_rows] reference (log2 units), sum
+  int rec_rows;     // query heads of a KV head, at most kKvRows
   int groups;       // groups of kKvRows query heads of a KV head
   int grid;         // CTAs of the split kernel
 };
@@ -65,7 +71,6 @@ cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvGatherParams& p, cudaStream_t s);
 cudaError_t launch_kv_select(const KvSelectParams& p, cudaStream_t s);
 cudaError_t launch_kv_decode(const KvDecodeParams& p, cudaStream_t s);
-int kv_decode_ctas_per_sm(int fmt, int d);
 
 #ifdef __CUDACC__
 // ------------------------------------------------------------------ 16-bit types

@@ -43,8 +43,28 @@ size_t kv_rope_bytes(const starkv_kv_layout* lay, int max_pages) {
   const int tiles = (max_pages * kPage + kTile - 1) / kTile;
   return static_cast<size_t>(kTile + tiles) * (lay->cfg.head_dim / 2) * sizeof(float2);
 }
-size_t kv_record_bytes(const starkv_kv_layout* lay) {
-  return static_cast<size_t>(kKvMaxCtas) * 2 * kKvRows * (lay->cfg.head_dim * sizeof(float) + sizeof(float2));
+int kv_groups(const starkv_kv_layout* lay) {
+  return (lay->cfg.n_q_heads / lay->cfg.n_kv_heads + kKvRows - 1) / kKvRows;
+}
+int kv_record_rows(const starkv_kv_layout* lay) {
+  const int G = lay->cfg.n_q_heads / lay->cfg.n_kv_heads;
+  return G < kKvRows ? G : kKvRows;
+}
+constexpr size_t kKvCounterBytes = 256;
+constexpr int kKvMaxBatch = 65535;                  // sequences of a decode call (the join's grid)
+constexpr int64_t kKvMostTiles = int64_t(1) << 30;  // the kernels number tiles in 32 bits
+
+// Tiles that a decode call may visit, and the most pieces it cuts them into (see the split kernel's list).
+int64_t kv_tiles(const starkv_kv_layout* lay, int64_t batch, int64_t max_pages) {
+  return batch * lay->cfg.n_kv_heads * kv_groups(lay) * max_pages * (kPage / kv_tile_tokens(lay->cfg.fmt));
+}
+int64_t kv_pieces(const starkv_kv_layout* lay, int64_t batch) {
+  return static_cast<int64_t>(kKvMaxCtas) * kKvWarps * (1 + kKvRounds) + batch * lay->cfg.n_kv_heads * kv_groups(lay);
+}
+// Workspace: the counter, the sums, then (reference, sum) of the records.
+size_t kv_record_bytes(const starkv_kv_layout* lay, int64_t batch) {
+  return kKvCounterBytes + static_cast<size_t>(kv_pieces(lay, batch)) * kv_record_rows(lay) *
+                               (lay->cfg.head_dim * sizeof(float) + sizeof(float2));
 }
 
 starkv_status check_kv_layout(const starkv_kv_layout* lay) {
@@ -66,7 +86,7 @@ starkv_status fill_pool(const starkv_kv_layout* lay, const void* cache, int64_t 
   const starkv_status st = check_kv_layout(lay);
   if (st != STARKV_OK) return st;
   if (max_pages < 1 || max_pages > (1 << 24)) return fail(STARKV_ERR_INVALID_ARG, "max_pages outside [1, 2^24]");
-  if (num_pages < 1) return fail(STARKV_ERR_INVALID_ARG, "num_pages < 1");
+  if (num_pages < 1 || num_pages > INT32_MAX) return fail(STARKV_ERR_INVALID_ARG, "num_pages outside [1, 2^31)");
   if (!cache || !block_table || !dev_status) return fail(STARKV_ERR_INVALID_ARG, "NULL pointer argument");
   if (misaligned(cache)) return fail(STARKV_ERR_INVALID_ARG, "cache must be 16-byte aligned");
   p.cache = const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(cache));
@@ -129,18 +149,21 @@ starkv_status starkv_kv_layout_init(const starkv_kv_config* cfg, starkv_kv_layou
   return STARKV_OK;
 }
 
-starkv_status starkv_kv_alloc(const starkv_kv_layout* lay, int64_t num_pages, int32_t max_pages,
-                              starkv_kv_sizes* out) {
+starkv_status starkv_kv_alloc(const starkv_kv_layout* lay, int64_t num_pages, int32_t batch,
+                              int32_t max_pages, starkv_kv_sizes* out) {
   const starkv_status st = check_kv_layout(lay);
   if (st != STARKV_OK) return st;
   if (!out) return fail(STARKV_ERR_INVALID_ARG, "out is NULL");
-  if (num_pages < 0) return fail(STARKV_ERR_INVALID_ARG, "num_pages < 0");
+  if (num_pages < 0 || batch < 0 || batch > kKvMaxBatch)
+    return fail(STARKV_ERR_INVALID_ARG, "num_pages < 0 or batch outside [0, 65535]");
   if (max_pages < 1 || max_pages > (1 << 24)) return fail(STARKV_ERR_INVALID_ARG, "max_pages outside [1, 2^24]");
   if (static_cast<uint64_t>(num_pages) > SIZE_MAX / static_cast<uint64_t>(lay->page_bytes))
     return fail(STARKV_ERR_INVALID_ARG, "num_pages * page_bytes does not fit in size_t");
   out->cache_bytes = static_cast<size_t>(num_pages) * lay->page_bytes;
   out->rope_table_bytes = kv_rope_bytes(lay, max_pages);
-  out->decode_workspace_bytes = kv_record_bytes(lay);
+  if (kv_tiles(lay, batch, max_pages) > kKvMostTiles)
+    return fail(STARKV_ERR_INVALID_ARG, "batch * n_kv_heads * max_pages too large for one decode call");
+  out->decode_workspace_bytes = kv_record_bytes(lay, batch);
   return STARKV_OK;
 }
 
@@ -289,7 +312,7 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   if (st != STARKV_OK) return st;
   const starkv_kv_decode_opts none = {};
   const starkv_kv_decode_opts& o = opts ? *opts : none;
-  if (batch < 0 || batch > 65535) return fail(STARKV_ERR_INVALID_ARG, "batch outside [0, 65535]");
+  if (batch < 0 || batch > kKvMaxBatch) return fail(STARKV_ERR_INVALID_ARG, "batch outside [0, 65535]");
   if (!(o.scale >= 0.f) || !std::isfinite(o.scale)) return fail(STARKV_ERR_INVALID_ARG, "scale must be finite and >= 0");
   if (o.window < 0 || o.max_ctas < 0 || o.reserved != 0)
     return fail(STARKV_ERR_INVALID_ARG, "window or max_ctas < 0, or reserved not 0");
@@ -303,7 +326,9 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   if (!q || !seq_lens || !out || !workspace) return fail(STARKV_ERR_INVALID_ARG, "NULL pointer argument");
   if (misaligned(q) || misaligned(out) || misaligned(workspace))
     return fail(STARKV_ERR_INVALID_ARG, "q, out and workspace must be 16-byte aligned");
-  if (workspace_bytes < kv_record_bytes(lay)) return fail(STARKV_ERR_WORKSPACE, "decode workspace too small");
+  if (kv_tiles(lay, batch, max_pages) > kKvMostTiles)
+    return fail(STARKV_ERR_INVALID_ARG, "batch * n_kv_heads * max_pages too large for one decode call");
+  if (workspace_bytes < kv_record_bytes(lay, batch)) return fail(STARKV_ERR_WORKSPACE, "decode workspace too small");
   int sms = 0;
   st = device_sms(sms);
   if (st != STARKV_OK) return st;
@@ -316,16 +341,18 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   p.scale2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.out = reinterpret_cast<uint16_t*>(out);
   p.lse = lse;
-  p.groups = (p.pool.H / p.pool.Hkv + kKvRows - 1) / kKvRows;
+  p.groups = kv_groups(lay);
   // as many CTAs as fit on the device, and no more than there can be pages
   const int64_t most = static_cast<int64_t>(batch) * p.pool.Hkv * p.groups * (sel && n_sel < max_pages ? n_sel : max_pages);
-  int64_t grid = static_cast<int64_t>(sms) * kv_decode_ctas_per_sm(p.pool.fmt, p.pool.d);
+  int64_t grid = 2 * static_cast<int64_t>(sms);
   if (o.max_ctas > 0 && o.max_ctas < grid) grid = o.max_ctas;
   if (grid > kKvMaxCtas) grid = kKvMaxCtas;
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
-  p.rec = reinterpret_cast<float*>(workspace);
-  p.rec_ml = reinterpret_cast<float2*>(p.rec + static_cast<size_t>(kKvMaxCtas) * 2 * kKvRows * p.pool.d);
+  p.counter = reinterpret_cast<unsigned long long*>(workspace);
+  p.rec = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + kKvCounterBytes);
+  p.rec_rows = kv_record_rows(lay);
+  p.rec_ml = reinterpret_cast<float2*>(p.rec + static_cast<size_t>(kv_pieces(lay, batch)) * p.rec_rows * p.pool.d);
   const cudaError_t e = launch_kv_decode(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv decode launch");
   return STARKV_OK;

@@ -12,12 +12,17 @@
 // (bf16) or 22 (fp16) at no further instruction.  tcgen05 would give the same products of 8 rows a
 // 128-row tile.
 //
-// Split: all (sequence, KV head, page) units of the batch form one list, and CTA i of N takes the
-// units [T i / N, T (i + 1) / N): equal shares whatever the lengths, known on the device alone.  A
-// CTA walks its share segment by segment (a segment = its part of one sequence and KV head); each
-// of its four warps takes 16 of a page's 64 tokens through a private cp.async ring, so that the
-// loads never wait for another warp.  A segment that is a whole sequence is written out at once,
-// else as a partial record, and the join adds the records of a sequence in page order.
+// Split: a warp works alone.  Its unit is a tile of 16 tokens (int8: 32) of one KV head; the tiles of
+// all sequences and KV heads form one list, cut into chunks of equal length wherever the sequences
+// begin, and a chunk's part of one sequence and head is a piece.  Lengths are known on the device only, so
+// every warp derives the list from them.  Chunks are the same whoever takes them, so results do not hang
+// on timing; who takes them does: warp w starts with chunk w and draws the next from a counter.  (Equal
+// static shares left SMs idle at the end: at 32 x 32768 tokens they ended between 497 and 646 us.)  A
+// piece that is a whole sequence is written out at once, else as a partial record, and the join adds the
+// records of a sequence in order.  Each warp has its own ring of tiles in shared memory, filled by
+// cp.async, and no barrier with another: four warps that shared a page met once per piece, 1.6 us of a CTA's
+// loads each.  (TMA copies of the same tiles, issued by one lane: no faster at 32 x 32768 tokens, 628 us
+// against 621, and slower for short ones, 22.1 us against 19.4 at a ragged fp16 batch.)
 #include "kv.cuh"
 
 namespace starkv {
@@ -25,6 +30,9 @@ namespace {
 
 constexpr float kLazy = 8.f;  // the reference follows the running maximum when that is 2^8 above it:
                               // weights stay below 2^8, and O is rescaled a few times per sequence
+constexpr unsigned kStatic = 40;    // tiles a warp below which there are large chunks only
+constexpr unsigned kDrawnPart = 4;  // one tile in so many belongs to a small chunk
+constexpr int kSmall = 8;           // tiles of a small chunk at least; at most kKvRounds of them a warp, about
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Weights of fp16 products are scaled by 2^7 (the factor is part of the reference): with kLazy they
@@ -92,23 +100,19 @@ __device__ __forceinline__ void cp_wait() {
 template <int FMT, int D>
 struct Ring {
   static constexpr bool kInt8 = FMT == STARKV_KV_INT8;
-  // Tokens of a warp's tile: 16, so that the four warps share every page; int8, whose time is
-  // instructions, 32, so that the steps of a tile that are not per token count half as much.
-  static constexpr int kTok = kInt8 ? 32 : 16;
-  static constexpr int kParts = kPage / kTok;          // warps that share a page
-  static constexpr int kPages = kKvWarps / kParts;     // pages that the CTA's warps take at a time
-  static constexpr int kRow = kInt8 ? D : 2 * D;            // bytes of a token's keys (or values)
-  static constexpr int kKeys = kTok * kRow;                 // one tile's keys
+  // Tokens of a tile: 16; int8, whose time is instructions, 32, so that the steps of a tile that are
+  // not per token count half as much.
+  static constexpr int kTok = kv_tile_tokens(FMT);
+  static constexpr int kParts = kPage / kTok;  // tiles of a page
+  static constexpr int kRow = kInt8 ? D : 2 * D;  // bytes of a token's keys (or values)
+  static constexpr int kKeys = kTok * kRow;       // one tile's keys
   static constexpr int kScales = kInt8 ? kTok * (D / 32) * 2 : 0;
   static constexpr int kStage = 2 * kKeys + 2 * kScales;
   static constexpr int kCtas = 2;  // per SM
-  static constexpr int kStages = kInt8 ? (D == 128 ? 2 : 5) : (D == 128 ? 3 : 6);
+  static constexpr int kStages = kInt8 ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 6);
   static constexpr int kBytes = kStage * kStages;
+  static constexpr int kSmem = kKvWarps * kBytes;
 };
-template <int FMT, int D>
-constexpr int smem_bytes() {
-  return kKvWarps * Ring<FMT, D>::kBytes + kKvWarps * kKvRows * D * 4 + kKvWarps * kKvRows * 8;
-}
 
 // Offset of a 16-byte chunk of a tile's row in shared memory: the chunks are permuted so that the
 // fragment loads touch every bank once.
@@ -119,7 +123,7 @@ __device__ __forceinline__ int chunk_at(int row, int c) {
   return row * D + (((c >> 1) ^ ((row >> 1) & 1)) << 5) + ((c & 1) << 4);
 }
 
-// ------------------------------------------------------------------ the list of units
+// ------------------------------------------------------------------ the list of tiles
 // Pages of a sequence that a call visits: [first, first + count) of the sequence, or count places
 // of its selection.
 struct Span {
@@ -134,124 +138,144 @@ __device__ __forceinline__ Span span_of(const KvDecodeParams& p, int b) {
   return s;
 }
 
-// Sum over the batch of the visited pages, and the part of it before sequence `stop` (whole warp).
-__device__ __forceinline__ long long sum_pages(const KvDecodeParams& p, int lane, int stop, long long& before) {
-  long long all = 0, part = 0;
-  for (int b = lane; b < p.pool.batch; b += 32) {
-    const int c = span_of(p, b).count;
-    all += c;
-    if (b < stop) part += c;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    part += __shfl_xor_sync(0xffffffffu, part, o);
-  }
-  before = part;
-  return all;
-}
-
-// x / y of non-negative numbers, by the short division where both fit.
-__device__ __forceinline__ long long quotient(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
-// A place in the list: sequence, KV head (and group of its query heads), page of the span.
-struct Cursor {
-  int b, hv, pg;
-  Span s;
-  __device__ __forceinline__ void next_segment(const KvDecodeParams& p, int heads) {
-    pg = 0;
-    if (++hv < heads) return;
-    hv = 0;
-    do {
-      ++b;
-      if (b >= p.pool.batch) return;
-      s = span_of(p, b);
-    } while (s.count == 0);
+// The list of tiles (at most 2^30: checked by the caller) and its chunks, the same in every warp and in
+// the join: one large chunk for each warp, then small ones that the warps draw as they get there.
+struct Cut {  // chunk i has base + 1 tiles where i < more, else base
+  int n, base, more;
+  __device__ __forceinline__ Cut() : n(0), base(1), more(0) {}
+  __device__ __forceinline__ Cut(unsigned tiles, unsigned chunks)
+      : n(chunks), base(tiles / chunks), more(tiles - chunks * (tiles / chunks)) {}
+  __device__ __forceinline__ int start(int i) const { return i * base + min(i, more); }
+  __device__ __forceinline__ int chunk_of(int u) const {
+    const int edge = more * (base + 1);
+    return u < edge ? u / (base + 1) : more + (u - edge) / base;
   }
 };
+struct List {
+  int n, edge;  // chunks, tiles of the large ones
+  Cut large, small;
+  __device__ __forceinline__ int start(int i) const {
+    return i < large.n ? large.start(i) : edge + small.start(i - large.n);
+  }
+  __device__ __forceinline__ int chunk_of(int u) const {
+    return u < edge ? large.chunk_of(u) : large.n + small.chunk_of(u - edge);
+  }
+};
+__device__ __forceinline__ List list_of(const KvDecodeParams& p, int lane, int per_page) {
+  unsigned all = 0;
+  for (int b = lane; b < p.pool.batch; b += 32) all += span_of(p, b).count;
+  all = __reduce_add_sync(0xffffffffu, all) * (p.pool.Hkv * p.groups * per_page);
+  List l;
+  l.n = l.edge = 0;
+  if (all == 0) return l;
+  const unsigned warps = p.grid * kKvWarps;
+  // SMs differ by a quarter in the bytes they get; below kStatic tiles a warp a share is too short to divide
+  const unsigned rest = all > warps * kStatic ? all / kDrawnPart : 0;
+  l.edge = all - rest;
+  l.large = Cut(all - rest, min(all, warps));
+  if (rest > 0) {
+    const unsigned size = max((rest + warps * kKvRounds - 1) / (warps * kKvRounds), (unsigned)kSmall);
+    l.small = Cut(rest, (rest + size - 1) / size);
+  }
+  l.n = l.large.n + l.small.n;
+  return l;
+}
 
-// A warp's tiles of a CTA's share: pages phase, phase + STEP, ... of every segment.
-template <int STEP>
-struct Walk {
-  Cursor c;        // the segment's first page
-  int n, i;        // pages of the segment, the warp's place among them
-  long long left;  // pages of the share from this segment on; 0: done
-  __device__ __forceinline__ void begin(const Cursor& at, long long share, int phase, const KvDecodeParams& p, int heads) {
-    c = at, left = share;
-    n = static_cast<int>(min((long long)(c.s.count - c.pg), left)), i = phase;
-    settle(phase, p, heads);
-  }
-  __device__ __forceinline__ void next(int phase, const KvDecodeParams& p, int heads) {
-    i += STEP;
-    settle(phase, p, heads);
-  }
-  __device__ __forceinline__ void settle(int phase, const KvDecodeParams& p, int heads) {
-    while (i >= n) {
-      left -= n;
-      if (left == 0) return;
-      c.next_segment(p, heads);
-      n = static_cast<int>(min((long long)c.s.count, left)), i = phase;
+// What a warp is loading: tiles of one piece.
+struct Piece {
+  int b, hv;            // sequence; KV head (and group of its query heads)
+  int chunk, chunk_left;  // its chunk, and the tiles left of that
+  int tile, left, size;   // next tile of the sequence's, tiles left of the piece, tiles of the sequence
+  Span s;
+  int page0, page, at;  // first page of the piece; of page `lane` of it: the block table's entry, and the
+                        // index in the sequence (-1: none)
+};
+
+// Page numbers of the piece, one per lane (whole warp).
+__device__ __forceinline__ void load_pages(const KvDecodeParams& p, Piece& c, int lane, int per_page) {
+  c.page0 = c.tile / per_page;
+  const int i = c.page0 + lane;
+  c.page = -1;
+  c.at = -1;
+  if (i < c.s.count && i * per_page < c.tile + c.left) {
+    c.at = c.s.first + i;
+    if (p.sel) c.at = p.sel[((long long)c.b * p.pool.Hkv + c.hv / p.groups) * p.n_sel + i];
+    if (c.at >= 0 && c.at < (c.s.len + kPage - 1) / kPage) {
+      c.page = p.pool.block_table[(long long)c.b * p.pool.max_pages + c.at];  // looked at by tile_of
+    } else if (c.at != -1) {
+      atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+      c.at = -1;
     }
   }
-};
+}
 
-// Place of unit u (whole warp; u below the total).
-__device__ __forceinline__ Cursor find(const KvDecodeParams& p, int lane, int heads, long long u) {
-  Cursor c;
-  long long before = 0;
+// The first piece of a chunk (whole warp).
+__device__ __forceinline__ Piece piece_of(const KvDecodeParams& p, const List& list, int lane, int per_page, int chunk) {
+  Piece c;
+  const int heads = p.pool.Hkv * p.groups;
+  const int u = list.start(chunk);
+  c.chunk = chunk;
+  c.chunk_left = list.start(chunk + 1) - u;
+  int before = 0;
   for (int b0 = 0;; b0 += 32) {
     const int b = b0 + lane;
-    const int n = b < p.pool.batch ? span_of(p, b).count : 0;
-    long long inc = n;
+    const int n = b < p.pool.batch ? span_of(p, b).count * heads * per_page : 0;
+    int inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, (before + inc) * heads > u);
-    if (m || b0 + 32 >= p.pool.batch) {
+    const unsigned m = __ballot_sync(0xffffffffu, before + inc > u);
+    if (m || b0 + 32 >= p.pool.batch) {  // found: u lies inside the list
       const int l = m ? __ffs(m) - 1 : 0;
       c.b = b0 + l;
-      const long long start = (before + __shfl_sync(0xffffffffu, inc - n, l)) * heads;
+      const int in = u - before - __shfl_sync(0xffffffffu, inc - n, l);
       c.s = span_of(p, c.b);
-      const long long in = u - start;
-      c.hv = static_cast<int>(quotient(in, max(c.s.count, 1)));
-      c.pg = static_cast<int>(in - (long long)c.hv * c.s.count);
-      return c;
+      c.size = c.s.count * per_page;
+      c.hv = in / c.size;
+      c.tile = in - c.hv * c.size;
+      break;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
+  c.left = min(c.size - c.tile, c.chunk_left);
+  load_pages(p, c, lane, per_page);
+  return c;
+}
+
+// The next piece of the same chunk.
+__device__ __forceinline__ void next_piece(const KvDecodeParams& p, Piece& c, int lane, int per_page) {
+  c.tile = 0;
+  if (++c.hv == p.pool.Hkv * p.groups) {
+    c.hv = 0;
+    do {
+      c.s = span_of(p, ++c.b);
+    } while (c.s.count == 0);
+    c.size = c.s.count * per_page;
+  }
+  c.left = min(c.size, c.chunk_left);
+  load_pages(p, c, lane, per_page);
 }
 
 // ------------------------------------------------------------------ loads
-// Where the warp's tile of the unit at a cursor lies, and which of its rows count: [lo, hi).
+// Where a tile lies, and which of its rows count: [lo, hi).
 struct Tile {
-  const uint8_t* src;  // the head's tile of the page, or null
+  const uint8_t* src;  // the head's tile of the page
   int lo, hi;
 };
 template <int TOK>
-__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Cursor& c, int pg, int part) {
+__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Piece& c, int part) {
   Tile t{nullptr, 0, 0};
-  const int g = c.hv / p.groups;
-  int i = c.s.first + pg;
-  if (p.sel) {
-    i = p.sel[((long long)c.b * p.pool.Hkv + g) * p.n_sel + pg];
-    if (i == -1) return t;
-    if (i < 0 || i >= (c.s.len + kPage - 1) / kPage) {
-      atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
-      return t;
-    }
-  }
-  uint8_t* page = kv_page(p.pool, c.b, i);
-  if (!page) {
+  const int i = c.tile / (kPage / TOK) - c.page0;
+  const int page = __shfl_sync(0xffffffffu, c.page, i), at = __shfl_sync(0xffffffffu, c.at, i);
+  if (at < 0) return t;
+  if (page < 0 || page >= p.pool.num_pages) {
     atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
     return t;
   }
-  t.src = page + p.pool.off_heads + (long long)g * p.pool.head_bytes;
-  const int t0 = i * kPage + part * TOK;
+  const int t0 = at * kPage + part * TOK;
+  t.src = p.pool.cache + page * p.pool.page_bytes + p.pool.off_heads + (long long)(c.hv / p.groups) * p.pool.head_bytes;
   t.hi = min(max(c.s.len - t0, 0), TOK);
   t.lo = p.window > 0 ? min(max(c.s.len - p.window - t0, 0), TOK) : 0;
   return t;
@@ -493,168 +517,174 @@ struct Sums {
     }
   }
 
-  // This warp's sums to shared memory: [row][D] and (m, l) per row.
-  __device__ __forceinline__ void put(float* os, float2* ml, int lane) {
+  // The sums of the piece of (b, hv): the result where it is the whole sequence, else a record.
+  __device__ __forceinline__ void end(const KvDecodeParams& p, int b, int hv, bool whole, int chunk, int lane) {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const int g = lane / 4, t = lane % 4;
-    if (t == 0) ml[g] = make_float2(m, l);
-    float* d = os + g * D;
-    if (!kInt8) {
+    const int r = lane / 4, t = lane % 4, G = p.pool.H / p.pool.Hkv;
+    const int head = hv % p.groups * kKvRows + r;  // of the KV head's
+    if (head >= G) return;
+    const long long row = (long long)b * p.pool.H + hv / p.groups * G + head;
+    const long long rec = ((long long)chunk + (long long)b * p.pool.Hkv * p.groups + hv) * p.rec_rows + r;
+    const float inv = m == __int_as_float(0xff800000) ? 0.f : 1.f / l;
+    if (t == 0) {
+      if (!whole) p.rec_ml[rec] = make_float2(m, l);
+      else if (p.lse) p.lse[row] = kLn2 * (m + log2f(l));
+    }
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D);
+    float2* part = reinterpret_cast<float2*>(p.rec + rec * D);
+    auto put = [&](int pair, float x, float y) {
+      if (whole) out[pair] = kv_pack<FMT>(x * inv, y * inv);
+      else part[pair] = make_float2(x, y);
+    };
+    if constexpr (!kInt8) {
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<float2*>(d + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+      for (int n = 0; n < D / 8; ++n) put(4 * n + t, o[n][0] + o[n][2], o[n][1] + o[n][3]);
     } else {
 #pragma unroll
       for (int jj = 0; jj < D / 64; ++jj)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          d[8 * (2 * t + 8 * jj) + i] = o[8 * jj + i][0] + o[8 * jj + i][2];
-          d[8 * (2 * t + 1 + 8 * jj) + i] = o[8 * jj + i][1] + o[8 * jj + i][3];
-        }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            put(4 * (2 * t + e + 8 * jj) + i / 2, o[8 * jj + i][e] + o[8 * jj + i][e + 2],
+                o[8 * jj + i + 1][e] + o[8 * jj + i + 1][e + 2]);
     }
   }
 };
-
-template <int FMT>
-__device__ __forceinline__ uint16_t to16(float x) {
-  return static_cast<uint16_t>(kv_pack<FMT>(x, 0.f));
-}
 
 // Weight of a part with reference m under the common reference M (-inf: nothing there).
 __device__ __forceinline__ float part_weight(float m, float M) {
   return m == __int_as_float(0xff800000) ? 0.f : ex2(m - M);
 }
 
+
+// The counter of chunks drawn: the upper half says that the lower is one.  The join leaves it at zero;
+// whatever else the workspace holds there before a first call, the tag is missing and the warps take
+// their chunks in a fixed order instead, with the same results.
+constexpr unsigned long long kTag = 0x73744b56ull << 32;
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_kernel(const KvDecodeParams p) {
   using R = Ring<FMT, D>;
   extern __shared__ __align__(128) uint8_t smem[];
+  // what the tile in a stage of a warp's ring is: sequence, KV head, chunk, and [lo, hi) with flags
+  __shared__ int4 s_what[kKvWarps][R::kStages];
+  constexpr int kFirst = 1 << 16, kLast = 1 << 17, kWhole = 1 << 18, kThere = 1 << 19;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t ring = smem_u32(smem) + warp * R::kBytes;
-  float* os = reinterpret_cast<float*>(smem + kKvWarps * R::kBytes);
-  float2* ml = reinterpret_cast<float2*>(os + kKvWarps * kKvRows * D);
-  const int heads = p.pool.Hkv * p.groups, G = p.pool.H / p.pool.Hkv;
+  const int worker = blockIdx.x * kKvWarps + warp, workers = gridDim.x * kKvWarps;
 
   pdl_wait();
   pdl_launch_dependents();
-  long long before;
-  const long long total = sum_pages(p, lane, 0, before) * heads;
-  const long long parts = min((long long)gridDim.x, total);  // no CTA without a unit has a record
-  if (blockIdx.x >= parts) return;
-  const long long u0 = quotient(total * blockIdx.x, parts), u1 = quotient(total * (blockIdx.x + 1), parts);
-  const int part = warp % R::kParts, phase = warp / R::kParts;
-  Cursor c = find(p, lane, heads, u0);  // consumer: start of the current segment
-  Walk<R::kPages> lead;                 // producer
-  lead.begin(c, u1 - u0, phase, p, heads);
-  long long to_do = u1 - u0;
-  int rows[R::kStages];  // [lo, hi) of the tiles in the ring, oldest first
-#pragma unroll
-  for (int i = 0; i < R::kStages; ++i) rows[i] = 0;
+  const List list = list_of(p, lane, R::kParts);
+  if (worker >= list.n) return;
+  Piece c = piece_of(p, list, lane, R::kParts, worker);
+  int drawn_for = 0;             // chunks drawn
+  unsigned long long drawn = 0;  // lane 0: the draw of the chunk after c's, made when c's begins
+  auto draw = [&]() {
+    ++drawn_for;
+    if (lane == 0 && list.n > workers) drawn = atomicAdd(p.counter, 1ull);
+  };
+  draw();
   int wr = 0, rd = 0;
-  auto issue = [&]() -> int {
-    int r = 0;
-    if (lead.left > 0) {
-      const Tile t = tile_of<R::kTok>(p, lead.c, lead.c.pg + lead.i, part);
-      if (t.lo < t.hi) {
-        load_tile<FMT, D>(p, t, ring + wr * R::kStage, part, lane);
-        r = t.lo | t.hi << 8;
+  bool first = true, whole = false;  // the next tile is its piece's first; the piece is a whole sequence
+  bool on = true;                    // there are tiles left
+  auto issue = [&]() {
+    int4 what = make_int4(0, 0, 0, 0);
+    if (on) {
+      const Tile t = tile_of<R::kTok>(p, c, c.tile % R::kParts);
+      if (t.lo < t.hi) load_tile<FMT, D>(p, t, ring + wr * R::kStage, c.tile % R::kParts, lane);
+      what = make_int4(c.b, c.hv, c.chunk, t.lo | t.hi << 8 | kThere);
+      if (first) what.w |= kFirst, whole = c.left == c.size;
+      if (whole) what.w |= kWhole;
+      first = false;
+      ++c.tile, --c.left, --c.chunk_left;
+      if (c.left == 0) {
+        what.w |= kLast;
+        first = true;
+        if (c.chunk_left > 0) {
+          next_piece(p, c, lane, R::kParts);
+        } else {
+          int id = list.n;
+          if (list.n > workers) {
+            const unsigned long long d = __shfl_sync(0xffffffffu, drawn, 0);
+            id = (d >> 32) == (kTag >> 32) ? workers + static_cast<int>(d & 0xffffffffull) : worker + drawn_for * workers;
+          }
+          on = id < list.n;
+          if (on) {
+            draw();
+            c = piece_of(p, list, lane, R::kParts, id);
+          }
+        }
+      } else if (c.tile == (c.page0 + 32) * R::kParts) {
+        load_pages(p, c, lane, R::kParts);
       }
-      lead.next(phase, p, heads);
     }
+    if (lane == 0) s_what[warp][wr] = what;
     cp_commit();
     wr = wr + 1 == R::kStages ? 0 : wr + 1;
-    return r;
   };
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) rows[i] = issue();
+  for (int i = 0; i < R::kStages - 1; ++i) issue();
 
   Sums<FMT, D> sums;
-  while (to_do > 0) {
-    const int n = static_cast<int>(min((long long)(c.s.count - c.pg), to_do));
-    sums.begin(p, c.b, c.hv, lane);
-    for (int i = phase; i < n; i += R::kPages) {
-      rows[R::kStages - 1] = issue();
-      cp_wait<R::kStages - 1>();
-      __syncwarp();
-      const int lo = rows[0] & 255, hi = rows[0] >> 8;
-      if (lo < hi) sums.add(ring + rd * R::kStage, lo, hi, lane);
-      __syncwarp();  // the stage is free for the next issue
-      rd = rd + 1 == R::kStages ? 0 : rd + 1;
-#pragma unroll
-      for (int k = 0; k + 1 < R::kStages; ++k) rows[k] = rows[k + 1];
-    }
-    // join the four warps
-    sums.put(os + warp * kKvRows * D, ml + warp * kKvRows, lane);
-    __syncthreads();
-    const int g = c.hv / p.groups, r0 = c.hv % p.groups * kKvRows, nr = min(G - r0, kKvRows);
-    const bool whole = n == c.s.count;
-    const long long slot = (long long)blockIdx.x * 2 + (c.pg == 0 ? 1 : 0);
-    for (int i = threadIdx.x; i < nr * D; i += 32 * kKvWarps) {
-      const int r = i / D, ch = i % D;
-      float M = __int_as_float(0xff800000);
-#pragma unroll
-      for (int w = 0; w < kKvWarps; ++w) M = fmaxf(M, ml[w * kKvRows + r].x);
-      float acc = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kKvWarps; ++w) {
-        const float f = part_weight(ml[w * kKvRows + r].x, M);
-        l = fmaf(f, ml[w * kKvRows + r].y, l);
-        acc = fmaf(f, os[(w * kKvRows + r) * D + ch], acc);
-      }
-      if (whole) {
-        const long long row = (long long)c.b * p.pool.H + g * G + r0 + r;
-        p.out[row * D + ch] = to16<FMT>(M == __int_as_float(0xff800000) ? 0.f : acc / l);
-        if (p.lse && ch == 0) p.lse[row] = kLn2 * (M + log2f(l));
-      } else {
-        p.rec[(slot * kKvRows + r) * D + ch] = acc;
-        if (ch == 0) p.rec_ml[slot * kKvRows + r] = make_float2(M, l);
-      }
-    }
-    __syncthreads();
-    to_do -= n;
-    if (to_do > 0) c.next_segment(p, heads);
+  for (;;) {
+    issue();
+    cp_wait<R::kStages - 1>();
+    __syncwarp();
+    const int4 what = s_what[warp][rd];
+    if (!(what.w & kThere)) break;
+    if (what.w & kFirst) sums.begin(p, what.x, what.y, lane);
+    const int lo = what.w & 255, hi = what.w >> 8 & 255;
+    if (lo < hi) sums.add(ring + rd * R::kStage, lo, hi, lane);
+    if (what.w & kLast) sums.end(p, what.x, what.y, what.w & kWhole, what.z, lane);
+    __syncwarp();  // the stage is free for the next issue
+    rd = rd + 1 == R::kStages ? 0 : rd + 1;
   }
+  cp_wait<0>();
 }
 
-// Joins the records of the sequences that several CTAs shared; writes zeros for empty ones.  One warp
-// per (sequence, query head), no shared memory, so that its CTAs can wait beside the split kernel's.  A
-// record is read by eight lanes (D / 8 channels each): four records a round, four rounds in flight.
+// Joins the records of the sequences that several chunks shared; writes zeros for empty ones.  One CTA
+// per (sequence, query head); a record is read by eight lanes (D / 8 channels each), so that the eight
+// warps read 32 records a round, four rounds in flight.
+constexpr int kJoinWarps = 8;
 template <int FMT, int D>
-__global__ void __launch_bounds__(32) kv_join_kernel(const KvDecodeParams p) {
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvDecodeParams p) {
   constexpr int N4 = D / 32;  // 16-byte loads of a lane's share of a record
-  const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x, part = lane % 8, sub = lane / 8;
+  __shared__ float s_l[kJoinWarps], s_acc[kJoinWarps][D];
+  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % 8;
   const int G = p.pool.H / p.pool.Hkv, heads = p.pool.Hkv * p.groups;
   const int g = h / G, hv = g * p.groups + h % G / kKvRows, r = h % G % kKvRows;
+  constexpr int per_page = Ring<FMT, D>::kParts;
   pdl_wait();
   pdl_launch_dependents();
+  if (threadIdx.x == 0 && h == 0 && b == 0) *p.counter = kTag;
   const long long row = (long long)b * p.pool.H + h;
   const int count = span_of(p, b).count;
-  if (lane == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
+  if (threadIdx.x == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
     atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
-  uint2* out = reinterpret_cast<uint2*>(p.out + row * D);
   if (count == 0) {
-    if (lane < D / 4) out[lane] = make_uint2(0, 0);
-    if (p.lse && lane == 0) p.lse[row] = __int_as_float(0xff800000);
+    if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(p.out + row * D)[threadIdx.x] = 0;
+    if (p.lse && threadIdx.x == 0) p.lse[row] = __int_as_float(0xff800000);
     return;
   }
-  long long before;
-  const long long total = sum_pages(p, lane, b, before) * heads;
-  const long long s0 = before * heads + (long long)hv * count, s1 = s0 + count;
-  // CTA i of N = min(grid, T) holds the units [T i / N, T (i + 1) / N): unit u lies in CTA
-  // ((u + 1) N - 1) / T
-  const long long parts = min((long long)p.grid, total);
-  const int c0 = static_cast<int>(quotient((s0 + 1) * parts - 1, total));
-  const int c1 = static_cast<int>(quotient(s1 * parts - 1, total));
+  // the chunks of this head's tiles
+  const List list = list_of(p, lane, per_page);
+  int before = 0;
+  for (int i = lane; i < b; i += 32) before += span_of(p, i).count;
+  before = __reduce_add_sync(0xffffffffu, before) * heads * per_page + hv * count * per_page;
+  const int c0 = list.chunk_of(before), c1 = list.chunk_of(before + count * per_page - 1);
   if (c0 == c1) return;
-  auto at = [&](int i) { return ((long long)i * 2 + (i == c0 ? 1 : 0)) * kKvRows + r; };
+  const long long rec0 = (long long)b * heads + hv;
+  auto at = [&](int i) { return (rec0 + i) * p.rec_rows + r; };
   float M = __int_as_float(0xff800000);
   for (int i = c0 + lane; i <= c1; i += 32) M = fmaxf(M, p.rec_ml[at(i)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float l = 0.f, acc[4 * N4] = {};
 #pragma unroll 4
-  for (int i = c0 + sub; i <= c1; i += 4) {
+  for (int i = c0 + threadIdx.x / 8; i <= c1; i += 4 * kJoinWarps) {
     const float2 x = p.rec_ml[at(i)];
     const float f = part_weight(x.x, M);
     l = fmaf(f, x.y, l);
@@ -672,30 +702,37 @@ __global__ void __launch_bounds__(32) kv_join_kernel(const KvDecodeParams p) {
 #pragma unroll
     for (int k = 0; k < 4 * N4; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
   }
-  const float inv = M == __int_as_float(0xff800000) ? 0.f : 1.f / l;
+  if (lane < 8) {
 #pragma unroll
-  for (int k = 0; k < N4; ++k)
-    if (sub == k % 4)
-      out[8 * k + part] = make_uint2(kv_pack<FMT>(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                                     kv_pack<FMT>(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-  if (p.lse && lane == 0) p.lse[row] = kLn2 * (M + log2f(l));
+    for (int k = 0; k < N4; ++k)
+      *reinterpret_cast<float4*>(&s_acc[warp][32 * k + 4 * part]) =
+          make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]);
+  }
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    float x = 0.f, y = 0.f;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      l += s_l[w];
+      x += s_acc[w][2 * threadIdx.x], y += s_acc[w][2 * threadIdx.x + 1];
+    }
+    const float inv = M == __int_as_float(0xff800000) ? 0.f : 1.f / l;
+    reinterpret_cast<uint32_t*>(p.out + row * D)[threadIdx.x] = kv_pack<FMT>(x * inv, y * inv);
+    if (p.lse && threadIdx.x == 0) p.lse[row] = kLn2 * (M + log2f(l));
+  }
 }
 
 template <int FMT, int D>
 cudaError_t decode_launch(const KvDecodeParams& p, cudaStream_t s) {
-  constexpr int smem = smem_bytes<FMT, D>();
-  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using R = Ring<FMT, D>;
+  static_assert(R::kCtas == 2 && 2 * (R::kSmem + 2048) <= 228 * 1024, "two CTAs share an SM's memory");
+  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), smem, s, p);
+  e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), R::kSmem, s, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_join_kernel<FMT, D>, dim3(p.pool.H, p.pool.batch), dim3(32), 0, s, p);
-}
-
-template <int FMT, int D>
-int ctas_per_sm() {
-  constexpr int n = Ring<FMT, D>::kCtas;
-  static_assert(n * (smem_bytes<FMT, D>() + 1024) <= 228 * 1024, "the CTAs of an SM share its memory");
-  return n;
+  return launch_pdl(kv_join_kernel<FMT, D>, dim3(p.pool.H, p.pool.batch), dim3(32 * kJoinWarps), 0, s, p);
 }
 
 }  // namespace
@@ -707,14 +744,6 @@ cudaError_t launch_kv_decode(const KvDecodeParams& p, cudaStream_t s) {
     case STARKV_KV_F16: return d == 64 ? decode_launch<STARKV_KV_F16, 64>(p, s) : decode_launch<STARKV_KV_F16, 128>(p, s);
     case STARKV_KV_INT8: return d == 64 ? decode_launch<STARKV_KV_INT8, 64>(p, s) : decode_launch<STARKV_KV_INT8, 128>(p, s);
     default: return cudaErrorInvalidValue;
-  }
-}
-
-int kv_decode_ctas_per_sm(int fmt, int d) {
-  switch (fmt) {
-    case STARKV_KV_BF16: return d == 64 ? ctas_per_sm<STARKV_KV_BF16, 64>() : ctas_per_sm<STARKV_KV_BF16, 128>();
-    case STARKV_KV_F16: return d == 64 ? ctas_per_sm<STARKV_KV_F16, 64>() : ctas_per_sm<STARKV_KV_F16, 128>();
-    default: return d == 64 ? ctas_per_sm<STARKV_KV_INT8, 64>() : ctas_per_sm<STARKV_KV_INT8, 128>();
   }
 }
 

@@ -445,6 +445,30 @@ def test_infinite_and_nan_values_reach_only_their_rows():
     assert torch.equal(out[0][ok], want[0][ok])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_workspace_needs_no_initial_values(fmt):
+    """Whatever the workspace holds, a count of another call's or nothing sensible, results are the same
+    bits; and a call of other sizes between changes nothing."""
+    c = Case(fmt, 8, 2, 128, [3000, 17, 20000, 640], seed=13)
+    c.fill()
+    o = Case("f16", 4, 4, 64, [5000, 100], seed=14)
+    o.fill()
+    q, qo = c.draw(4, 8, 1.5), o.draw(2, 4)
+    out, lse = c.decode(q)
+    c.check(q, out, lse)
+    ws = c.kv.decode_ws
+    for i, fill in enumerate((0x00, 0xFF, 0x80, None)):
+        if fill is None:
+            ws.copy_(torch.randint(0, 256, ws.shape, dtype=torch.uint8, device="cuda"))
+        else:
+            ws.fill_(fill)
+        for _ in range(3):
+            again, lse2 = c.decode(q)
+            assert torch.equal(out, again) and torch.equal(lse, lse2), (i, _)
+            o.kv.decode_ws = ws
+            o.decode(qo)
+
+
 # ---------------------------------------------------------------------------------------- selection
 @pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
 @pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (4, 4, 64), (10, 2, 128), (3, 1, 64), (32, 2, 64), (20, 1, 128),

@@ -40,15 +40,20 @@ def test_struct_sizes(lib):
 
 def test_alloc_sizes(lib):
     lay = layout()
-    s = api.kv_alloc(lay, 7, 5)
+    s = api.kv_alloc(lay, 7, 3, 70)
     assert s.cache_bytes == 7 * lay.page_bytes
     # the table of the latent cache at the same head_dim and length
-    assert s.rope_table_bytes == (128 + 3) * 64 * 8
-    # two records of eight heads for each of 512 CTAs, whatever the batch
-    assert s.decode_workspace_bytes == 512 * 2 * 8 * (128 * 4 + 8)
-    for pages, width in ((-1, 1), (1, 0), (1, (1 << 24) + 1), (1 << 62, 1)):
+    assert s.rope_table_bytes == (128 + 35) * 64 * 8
+    # a record of four heads for each piece: nine chunks for each of 296 x 4 warps, and one more where
+    # each of 3 x 2 (sequence, KV head) ends; a counter before them
+    assert s.decode_workspace_bytes == 256 + (296 * 4 * 9 + 3 * 2) * 4 * (128 * 4 + 8)
+    # twenty query heads per KV head: three groups of at most eight
+    s = api.kv_alloc(layout("bf16", 40, 2, 64), 1, 5, 32)
+    assert s.decode_workspace_bytes == 256 + (296 * 4 * 9 + 5 * 2 * 3) * 8 * (64 * 4 + 8)
+    for args in ((-1, 1, 1), (1, 1, 0), (1, 1, (1 << 24) + 1), (1 << 62, 1, 1), (1, -1, 1), (1, 65536, 1),
+                 (1, 65535, 1 << 13)):
         with pytest.raises(L.StarkvError) as e:
-            api.kv_alloc(lay, pages, width)
+            api.kv_alloc(lay, *args)
         assert e.value.status == L.ERR_INVALID_ARG
 
 
@@ -71,7 +76,7 @@ def test_tampered_layout_rejected(lib):
     lay = layout()
     lay.head_bytes += 16
     with pytest.raises(L.StarkvError) as e:
-        api.kv_alloc(lay, 1, 1)
+        api.kv_alloc(lay, 1, 1, 1)
     assert e.value.status == L.ERR_INVALID_ARG
 
 
