@@ -12,6 +12,8 @@ constexpr int kKvWarps = 4;        // warps of a split CTA
 // Tokens of a tile, a warp's step (see the split kernel).
 constexpr int kv_tile_tokens(int fmt) { return fmt == STARKV_KV_INT8 ? 32 : 16; }
 
+constexpr int kSelMaxCluster = 16;  // CTAs that share the choice for one (sequence, KV head)
+
 // Where a token or page lies (offsets as in starkv_kv_layout).
 struct KvPool {
   uint8_t* cache;

@@ -293,10 +293,10 @@ starkv_status starkv_kv_select(const starkv_kv_layout* lay, const void* q, const
   p.keep_first = keep_first;
   p.keep_last = keep_last;
   p.sel = sel;
-  // CTAs per (sequence, KV head): enough to cover the device, none without a round of pages
+  // CTAs per (sequence, KV head): four of them fit on an SM; none without a round of pages (64)
   const int64_t units = static_cast<int64_t>(batch) * p.pool.Hkv;
   p.cluster = 1;
-  while (p.cluster < 8 && units * p.cluster < 2 * sms && p.cluster * 64 < max_pages) p.cluster *= 2;
+  while (p.cluster < kSelMaxCluster && units * p.cluster * 2 <= 4 * sms && p.cluster * 64 < max_pages) p.cluster *= 2;
   const cudaError_t e = launch_kv_select(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv select launch");
   return STARKV_OK;

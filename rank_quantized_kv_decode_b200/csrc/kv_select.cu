@@ -7,10 +7,11 @@
 // hang on the order of a summation, and equal pages score equally.
 //
 // Two steps give that choice at the cost of fp32.  (1) All scores in fp32 on mma.sync (16 pages and all
-// heads of a KV head a round, 4 d / 16 products), with a bound e of their error.  (2) With v the n-th
-// largest, the n-th largest exact score lies within e of v: pages above v + 2 e are in, pages below
-// v - 2 e are out, and only those between are scored again in fp64 and ranked.  fp64 throughout
-// took 65 us at 32 sequences x 512 pages x 8 KV heads (170 registers, one CTA per SM).
+// heads of a KV head a round, 4 d / 16 products), with a bound e of their error.  (2) A histogram finds
+// the bin [v0, v1] of the n-th largest; the n-th largest exact score lies in [v0 - e, v1 + e], so pages
+// above v1 + 2 e are in, pages below v0 - 2 e are out, and only those between (a few) are scored again in
+// fp64 and ranked.  fp64 throughout took 65 us at 32 sequences x 512 pages x 8 KV heads; finding the n-th
+// largest bit by bit 4 us of a sequence's 17, the histogram 1.
 //
 // Bound: HBM for large batches (the bounds are 4 d bytes per page and KV head, read once), latency
 // for one sequence.  A cluster of CTAs shares one (sequence, KV head): each scores its share of the
@@ -22,13 +23,14 @@
 namespace starkv {
 namespace {
 
-constexpr int kSelThreads = 256;
+constexpr int kSelThreads = 128;
+constexpr int kBins = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 // Error of an fp32 score over S = sum |q_c| |b_c|: d / 8 products of 16 terms accumulate, each losing at
 // most 17 x 2^-24 of the running magnitude (<= S) where the unit cuts instead of rounding: 16 x 17 x
 // 2^-24 < 2^-15.9 at d = 128.
 constexpr float kScoreError = 1.f / 32768.f;
-constexpr int kRankAll = 256;  // pages between that are ranked by comparing all pairs
+constexpr int kRankAll = kSelThreads;  // pages between that are ranked by comparing all pairs
 
 template <bool BF>
 __device__ __forceinline__ void mma_score(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
@@ -45,6 +47,10 @@ __device__ __forceinline__ void mma_score(float (&c)[4], uint32_t a0, uint32_t a
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1));
 }
+
+// Shared memory of a CTA: exact keys or the histogram, fp32 keys, list of pages.
+__host__ __device__ constexpr int exact_bytes(int max_pages) { return max_pages * 8 > kBins * 4 ? max_pages * 8 : kBins * 4; }
+constexpr int select_smem(int max_pages) { return exact_bytes(max_pages) + max_pages * (4 + 2); }
 
 // The negative 16-bit halves of a word, and the rest.
 __device__ __forceinline__ uint32_t negatives(uint32_t w) {
@@ -77,47 +83,49 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k);
 }
 
-// Exact score of a page (whole warp): the sum scaled by a power of two, the same for all pages.
+// Exact bound of one query head over a page, scaled by a power of two, the same for all pages: eight
+// lanes, D / 8 channels each (part = lane % 8); the whole warp shuffles.
 template <int F, int D>
-__device__ double exact_score(const KvPool& P, const uint16_t* q, int G, const uint8_t* bounds, int lane) {
-  constexpr int W = D / 64;  // words (channel pairs) of a lane
-  double best = -__longlong_as_double(0x7ff0000000000000ll);
-  const uint32_t* lo = reinterpret_cast<const uint32_t*>(bounds) + lane * W;
-  uint32_t l[W], u[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) l[i] = lo[i], u[i] = lo[D / 2 + i];
+__device__ __forceinline__ double exact_bound(const uint16_t* q, const uint8_t* bounds, int part) {
+  constexpr int W = D / 64;  // 16-byte loads of a lane
   // undoes field_double's factor, up to a power of two that keeps the largest query finite
   const double up = __hiloint2double((1023 + (F == STARKV_KV_F16 ? 1000 : 880)) << 20, 0);
-  for (int h = 0; h < G; ++h) {
-    double a = 0.0;
+  double a = 0.0, z = 0.0;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 x = kv_unpack<F>(reinterpret_cast<const uint32_t*>(q + h * D)[lane * W + i]);
+  for (int j = 0; j < W; ++j) {
+    const uint4 l4 = reinterpret_cast<const uint4*>(bounds)[8 * j + part];
+    const uint4 u4 = reinterpret_cast<const uint4*>(bounds)[8 * j + part + D / 8];
+    const uint4 q4 = reinterpret_cast<const uint4*>(q)[8 * j + part];
+    const uint32_t l[4] = {l4.x, l4.y, l4.z, l4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w}, w[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = kv_unpack<F>(w[i]);
       a = fma(x.x * up, field_double<F>((x.x < 0.f ? l[i] : u[i]) << 16), a);
-      a = fma(x.y * up, field_double<F>((x.y < 0.f ? l[i] : u[i]) & 0xffff0000u), a);
+      z = fma(x.y * up, field_double<F>((x.y < 0.f ? l[i] : u[i]) & 0xffff0000u), z);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    best = fmax(best, a);
   }
-  return best;
+  a += z;
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  return a;
 }
 
 template <int F, int D>
-__global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelectParams p) {
   constexpr int NJ = D / 32;   // 16-byte loads per row and lane
   constexpr int RP = 16;       // pages of a warp's round
   extern __shared__ __align__(16) uint8_t smem[];
   const KvPool& P = p.pool;
-  // in the cluster's first CTA: exact keys of the pages between, fp32 keys of all, the pages between
+  // in the cluster's first CTA: exact keys of the pages between (before them the histogram), fp32 keys
+  // of all pages, the pages between
   unsigned long long* keys64 = reinterpret_cast<unsigned long long*>(smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(keys64 + P.max_pages);
+  int* s_bins = reinterpret_cast<int*>(smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + exact_bytes(P.max_pages));
   uint16_t* list = reinterpret_cast<uint16_t*>(keys + P.max_pages);
-  __shared__ uint32_t s_mag[8];      // largest magnitude of a bound, per CTA of the cluster
-  __shared__ uint32_t s_cnt[2][2][kSelWarps];
+  __shared__ uint32_t s_mag[kSelMaxCluster];  // largest magnitude of a bound, per CTA of the cluster
+  __shared__ uint32_t s_cnt[2][kSelWarps];
   __shared__ uint32_t s_ext[2][kSelWarps];
-  __shared__ float s_q1[kSelWarps];
-  __shared__ int s_m, s_in;
+  __shared__ int s_m, s_in, s_bin;
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = blockIdx.x % p.cluster, unit = blockIdx.x / p.cluster;
@@ -145,13 +153,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
     return;
   }
 
-  // ---- fp32 scores
+  // ---- fp32 scores, and the largest sum |q_c| of a head (every warp for itself)
+  float q1 = 0.f;
   {
     uint32_t* first = cluster.map_shared_rank(keys, 0);
     uint32_t mag = 0;
+    for (int i = threadIdx.x; i < kBins; i += kSelThreads) s_bins[i] = 0;
     for (int h0 = 0; h0 < G; h0 += 8) {
       // A fragments: row = head (a head beyond the last stands twice), the lane's channels 8 (t + 4 j) + 0..7
       uint32_t qp[NJ][4], qn[NJ][4];
+      float head_sum = 0.f;
       const uint16_t* src = q + min(h0 + row, G - 1) * D + 8 * t;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
@@ -161,24 +172,36 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
         for (int i = 0; i < 4; ++i) {
           qn[j][i] = negatives(a[i]);
           qp[j][i] = a[i] ^ qn[j][i];
+          const float2 x = kv_unpack<F>(a[i]);
+          head_sum += fabsf(x.x) + fabsf(x.y);
         }
       }
-      for (int i0 = (rank * kSelWarps + warp) * RP; i0 < nc; i0 += p.cluster * kSelWarps * RP) {
+      head_sum += __shfl_xor_sync(0xffffffffu, head_sum, 1);
+      head_sum += __shfl_xor_sync(0xffffffffu, head_sum, 2);
+      q1 = fmaxf(q1, head_sum);
+      const int step = p.cluster * kSelWarps * RP;
+      const int* table = P.block_table + (long long)b * P.max_pages + c0;
+      int i0 = (rank * kSelWarps + warp) * RP, pid[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) pid[k] = i0 + 8 * k + row < nc ? table[i0 + 8 * k + row] : 0;
+      for (; i0 < nc; i0 += step) {
         uint4 lo[2][NJ], hi[2][NJ];
         bool have[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const int i = i0 + 8 * k + row;
-          const uint8_t* page = i < nc ? kv_page(P, b, c0 + i) : nullptr;
-          have[k] = page != nullptr;
-          if (!page && i < nc && t == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
-          const uint4* x = reinterpret_cast<const uint4*>(page + (long long)g * 4 * D) + t;
+          const bool in = i0 + 8 * k + row < nc;
+          have[k] = in && pid[k] >= 0 && pid[k] < P.num_pages;
+          if (in && !have[k] && t == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
+          const uint4* x = reinterpret_cast<const uint4*>(P.cache + pid[k] * P.page_bytes + (long long)g * 4 * D) + t;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
-            lo[k][j] = page ? x[4 * j] : make_uint4(0, 0, 0, 0);
-            hi[k][j] = page ? x[4 * j + D / 8] : make_uint4(0, 0, 0, 0);
+            lo[k][j] = have[k] ? x[4 * j] : make_uint4(0, 0, 0, 0);
+            hi[k][j] = have[k] ? x[4 * j + D / 8] : make_uint4(0, 0, 0, 0);
           }
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)  // the next round's pages
+          if (i0 + step + 8 * k + row < nc) pid[k] = table[i0 + step + 8 * k + row];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float c[4] = {}, z[4] = {};
@@ -226,104 +249,85 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
   cluster.sync();
   if (rank != 0) return;
 
-  // ---- error bound: kScoreError times the largest sum |q_c| of a head times the largest |bound|
+  // ---- the bin of the want-th largest key
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) q1 = fmaxf(q1, __shfl_xor_sync(0xffffffffu, q1, o));
+  uint32_t mn = 0xffffffffu, mx = 0;
+  for (int i = threadIdx.x; i < nc; i += kSelThreads) mn = min(mn, keys[i]), mx = max(mx, keys[i]);
+  mn = __reduce_min_sync(0xffffffffu, mn), mx = __reduce_max_sync(0xffffffffu, mx);
+  if (lane == 0) s_ext[0][warp] = mn, s_ext[1][warp] = mx;
+  if (threadIdx.x == 0) s_m = 0, s_in = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) mn = min(mn, s_ext[0][w]), mx = max(mx, s_ext[1][w]);
+  // the first shift by which all keys fall into kBins bins
+  const int shift = max(0, 32 - __clz(mx - mn) - (31 - __clz(kBins)));
+  for (int i = threadIdx.x; i < nc; i += kSelThreads) atomicAdd(&s_bins[(keys[i] - mn) >> shift], 1);
+  __syncthreads();
   {
-    float q1 = 0.f;
-    for (int h = warp; h < G; h += kSelWarps) {
-      float a = 0.f;
-      for (int c = lane; c < D / 2; c += 32) {
-        const float2 x = kv_unpack<F>(reinterpret_cast<const uint32_t*>(q + h * D)[c]);
-        a += fabsf(x.x) + fabsf(x.y);
-      }
+    constexpr int kOf = kBins / kSelThreads;  // bins of a thread, from the highest
+    int bins[kOf], sum = 0;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-      q1 = fmaxf(q1, a);
+    for (int i = 0; i < kOf; ++i) sum += bins[i] = s_bins[kBins - 1 - (kOf * threadIdx.x + i)];
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
     }
-    if (lane == 0) s_q1[warp] = q1;
-    if (threadIdx.x == 0) s_m = 0, s_in = 0;
-  }
-  // sums over the CTA, two buffers in turn: one barrier each
-  int buf = 0;
-  auto total2 = [&](uint32_t x, uint32_t y, uint32_t& sx, uint32_t& sy) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    y = __reduce_add_sync(0xffffffffu, y);
-    if (lane == 0) s_cnt[buf][0][warp] = x, s_cnt[buf][1][warp] = y;
+    if (lane == 31) s_cnt[0][warp] = inc;
     __syncthreads();
-    sx = sy = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) sx += s_cnt[buf][0][w], sy += s_cnt[buf][1][w];
-    buf ^= 1;
-  };
-
-  // ---- v, the want-th largest fp32 key: two bits a round from the first that differs
-  uint32_t vkey;
-  {
-    uint32_t mn = 0xffffffffu, mx = 0;
-    for (int i = threadIdx.x; i < nc; i += kSelThreads) mn = min(mn, keys[i]), mx = max(mx, keys[i]);
-    mn = __reduce_min_sync(0xffffffffu, mn), mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) s_ext[0][warp] = mn, s_ext[1][warp] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) mn = min(mn, s_ext[0][w]), mx = max(mx, s_ext[1][w]);
-    uint32_t thr = mx;
-    int high = 31 - __clz(mn ^ mx);  // -1: all equal
-    if (high >= 0) {
-      high |= 1;  // whole pairs of bits
-      thr = high < 31 ? mx & ~((2u << high) - 1) : 0u;
-      bool done = false;
-      for (int bit = high - 1; bit >= 0 && !done; bit -= 2) {
-        const uint32_t t1 = thr | 1u << bit, t2 = thr | 2u << bit, t3 = thr | 3u << bit;
-        uint32_t n12 = 0, n3 = 0;  // at most 16384 keys: two counts in a word
-        for (int i = threadIdx.x; i < nc; i += kSelThreads) {
-          const uint32_t k = keys[i];
-          n12 += (k >= t1) + ((k >= t2) << 16);
-          n3 += k >= t3;
-        }
-        uint32_t s12, s3;
-        total2(n12, n3, s12, s3);
-        const uint32_t s1 = s12 & 0xffffu, s2 = s12 >> 16, w = want;
-        thr = s3 >= w ? t3 : s2 >= w ? t2 : s1 >= w ? t1 : thr;
-        done = s1 == w || s2 == w || s3 == w;  // the chosen one has exactly `want` keys
-      }
+    int above = inc - sum;
+    for (int w = 0; w < warp; ++w) above += s_cnt[0][w];
+    if (above < want && want <= above + sum) {  // one thread
+      int i = 0;
+      for (; above + bins[i] < want; ++i) above += bins[i];
+      s_bin = kBins - 1 - (kOf * threadIdx.x + i);
     }
-    mn = 0xffffffffu;
-    for (int i = threadIdx.x; i < nc; i += kSelThreads)
-      if (keys[i] >= thr) mn = min(mn, keys[i]);
-    mn = __reduce_min_sync(0xffffffffu, mn);
     __syncthreads();
-    if (lane == 0) s_ext[0][warp] = mn;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) mn = min(mn, s_ext[0][w]);
-    vkey = mn;
   }
 
   // ---- in, out or between
   {
+    const uint32_t k0 = mn + (static_cast<uint32_t>(s_bin) << shift), width = (1u << shift) - 1;
+    const uint32_t k1 = mx - k0 < width ? mx : k0 + width;  // the bin's keys: [k0, k1]
     uint32_t mag = 0;
     for (int r = 0; r < p.cluster; ++r) mag = max(mag, s_mag[r]);
-    float q1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) q1 = fmaxf(q1, s_q1[w]);
     const float e2 = 2.f * kScoreError * q1 * kv_unpack<F>(mag).x;
-    // a bad page has key 0, below every score; where v itself is one, they all tie
-    const float v = vkey ? key_value(vkey) : 0.f;
-    for (int i = threadIdx.x; i < nc; i += kSelThreads) {
-      const uint32_t k = keys[i];
-      const float s = key_value(k);
-      const bool in = vkey == 0 ? k > 0 : (k > 0 && s > v + e2);
-      const bool out = vkey == 0 ? false : (k == 0 || s < v - e2);
-      keys[i] = in ? 0xffffffffu : 0u;
-      if (in) atomicAdd(&s_in, 1);
-      if (!in && !out) list[atomicAdd(&s_m, 1)] = static_cast<uint16_t>(i);
+    const float v0 = key_value(max(k0, 1u)), v1 = key_value(max(k1, 1u));
+    int ins = 0;
+    constexpr int kAt = 4;  // keys a thread has in hand
+    for (int i0 = threadIdx.x; i0 < nc; i0 += kAt * kSelThreads) {
+      uint32_t k[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) k[j] = i0 + j * kSelThreads < nc ? keys[i0 + j * kSelThreads] : 0u;
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const int i = i0 + j * kSelThreads;
+        if (i >= nc) break;
+        const float x = key_value(k[j]);
+        // a bad page has key 0, below every score: among themselves they tie, and are between where the
+        // bin reaches down to them
+        const bool in = k[j] > k1 && x > v1 + e2;
+        const bool out = k[j] == 0 ? k0 > 0 : (k[j] < k0 && x < v0 - e2);
+        keys[i] = in ? 0xffffffffu : 0u;
+        ins += in;
+        if (!in && !out) list[atomicAdd(&s_m, 1)] = static_cast<uint16_t>(i);
+      }
     }
+    ins = __reduce_add_sync(0xffffffffu, ins);
+    if (lane == 0 && ins) atomicAdd(&s_in, ins);
   }
   __syncthreads();
   const int m = s_m, need = want - s_in;  // 1 <= need <= m
-  for (int e = warp; e < m; e += kSelWarps) {
+  for (int e = threadIdx.x; e < m; e += kSelThreads) keys64[e] = 0ull;  // a bad page's stays
+  __syncthreads();
+  for (int i0 = 4 * warp; i0 < m * G; i0 += 4 * kSelWarps) {  // four (page, head) a round
+    const int i = min(i0 + lane / 8, m * G - 1), e = i / G, h = i - e * G;
     const uint8_t* page = kv_page(P, b, c0 + list[e]);
-    const double x = page ? exact_score<F, D>(P, q, G, page + (long long)g * 4 * D, lane) : 0.0;
-    if (lane == 0) keys64[e] = page ? order_key(x) : 0ull;
+    const uint8_t* bounds = page ? page + (long long)g * 4 * D : P.cache;  // read, but not used
+    const double x = exact_bound<F, D>(q + h * D, bounds, lane % 8);
+    if (lane % 8 == 0 && page) atomicMax(&keys64[e], order_key(x));
   }
   __syncthreads();
   if (m <= kRankAll) {
@@ -337,27 +341,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
   } else {
     // many pages tie (or nearly): the need-th largest exact key, then the lowest pages at it
     unsigned long long thr = 0;
-    uint32_t n, dummy;
+    int n, buf = 0;
+    auto total = [&](int x) {  // over the CTA, two buffers in turn: one barrier each
+      x = __reduce_add_sync(0xffffffffu, x);
+      if (lane == 0) s_cnt[buf][warp] = x;
+      __syncthreads();
+      x = 0;
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) x += s_cnt[buf][w];
+      buf ^= 1;
+      return x;
+    };
     bool exact = false;
     for (int bit = 63; bit >= 0 && !exact; --bit) {
       const unsigned long long cand = thr | 1ull << bit;
       n = 0;
       for (int e = threadIdx.x; e < m; e += kSelThreads) n += keys64[e] >= cand;
-      total2(n, 0, n, dummy);
-      if ((int)n >= need) thr = cand;
-      exact = (int)n == need;
+      n = total(n);
+      if (n >= need) thr = cand;
+      exact = n == need;
     }
     n = 0;
     for (int e = threadIdx.x; e < m; e += kSelThreads) n += keys64[e] > thr;
-    total2(n, 0, n, dummy);
-    const int at = need - static_cast<int>(n);  // pages to take at thr
+    n = total(n);
+    const int at = need - n;  // pages to take at thr
     int bound = 0;                              // those with an index below the largest bound that holds <= at
     for (int bit = 14; bit >= 0; --bit) {
       const int cand = bound | 1 << bit;
       n = 0;
       for (int e = threadIdx.x; e < m; e += kSelThreads) n += keys64[e] == thr && list[e] < cand;
-      total2(n, 0, n, dummy);
-      if ((int)n <= at) bound = cand;
+      n = total(n);
+      if (n <= at) bound = cand;
     }
     for (int e = threadIdx.x; e < m; e += kSelThreads)
       if (keys64[e] > thr || (keys64[e] == thr && list[e] < bound)) keys[list[e]] = 0xffffffffu;
@@ -365,7 +379,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
   __syncthreads();
 
   // ---- the chosen pages in order: a thread takes a run of candidates
-  const int per = (nc + kSelThreads - 1) / kSelThreads, i0 = min((int)threadIdx.x * per, nc), i1 = min(i0 + per, nc);
+  const int per = (nc + kSelThreads - 1) / kSelThreads | 1;  // odd: a run's stride meets every bank
+  const int i0 = min((int)threadIdx.x * per, nc), i1 = min(i0 + per, nc);
   int mine = 0;
   for (int i = i0; i < i1; ++i) mine += keys[i] != 0;
   int inc = mine;
@@ -374,23 +389,22 @@ __global__ void __launch_bounds__(kSelThreads, 2) kv_select_kernel(const KvSelec
     const int x = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += x;
   }
-  if (lane == 31) s_cnt[buf][0][warp] = inc;
+  if (lane == 31) s_cnt[0][warp] = inc;
   __syncthreads();
   int at = c0 + inc - mine;
-  for (int w = 0; w < warp; ++w) at += s_cnt[buf][0][w];
+  for (int w = 0; w < warp; ++w) at += s_cnt[0][w];
   for (int i = i0; i < i1; ++i)
     if (keys[i]) sel[at++] = c0 + i;
   for (int i = threadIdx.x; i < p.keep_first; i += kSelThreads) sel[i] = i;
   for (int i = threadIdx.x; i < p.keep_last; i += kSelThreads) sel[p.n_sel - p.keep_last + i] = pages - p.keep_last + i;
 }
 
-constexpr int select_smem(int max_pages) { return max_pages * (8 + 4 + 2); }
-
 template <int F, int D>
 cudaError_t select_launch(const KvSelectParams& p, cudaStream_t s) {
   auto kern = kv_select_kernel<F, D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        select_smem(STARKV_KV_MAX_SELECT_PAGES));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.pool.batch * p.pool.Hkv * p.cluster));
