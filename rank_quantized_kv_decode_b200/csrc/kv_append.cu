@@ -11,14 +11,14 @@ namespace starkv {
 namespace {
 
 constexpr int kAppendWarps = 8;
-constexpr int kRounds = 2;            // rounds of a warp's task, their loads in flight together
+constexpr int kRounds16 = 6, kRoundsInt8 = 3;  // rounds of a task of many tokens
 constexpr int kFusedBoundsMax = 256;  // tokens up to which one launch does both (see launch below)
 
 // A row is one head of q, k or v of a token; D/16 lanes share it, lane j with channels [8j, 8j+8) of
 // each half: both members of a pair, 16-byte accesses, and a scale group is four neighbouring lanes.
 template <int D>
 struct RowMap {
-  static constexpr int kLanes = D / 16, kRows = 32 / kLanes, kTask = kRows * kRounds;
+  static constexpr int kLanes = D / 16, kRows = 32 / kLanes;
 };
 
 struct Raw {
@@ -41,6 +41,25 @@ __device__ __forceinline__ void angles(const float2* rope, int pos, int j, float
     c[2 * i + 1] = make_float2(x.z * y.z - x.w * y.w, x.z * y.w + x.w * y.z);
   }
 }
+
+// Smaller and larger of two pairs of 16-bit values (a NaN gives way).
+template <int FMT>
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (FMT == STARKV_KV_F16) asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (FMT == STARKV_KV_F16) asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// +inf and -inf twice: what a minimum and a maximum begin with.
+template <int FMT>
+constexpr uint32_t kPairInf = FMT == STARKV_KV_F16 ? 0x7c007c00u : 0x7f807f80u;
 
 template <int FMT>
 struct Row {
@@ -67,9 +86,10 @@ struct Row {
     for (int i = 0; i < 4; ++i) a[i] = kv_pack<FMT>(lo[2 * i], lo[2 * i + 1]), z[i] = kv_pack<FMT>(hi[2 * i], hi[2 * i + 1]);
     return {make_uint4(a[0], a[1], a[2], a[3]), make_uint4(z[0], z[1], z[2], z[3])};
   }
-  // Scales of the lane's two groups (whole warp).
-  __device__ __forceinline__ void scales(__half& sa, __half& sz) const {
-    float ma = 0.f, mz = 0.f;
+  float ma, mz;  // largest magnitudes of the lane's two groups
+  // Scales of those groups (whole warp).
+  __device__ __forceinline__ void scales(__half& sa, __half& sz) {
+    ma = mz = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ma = fmaxf(ma, fabsf(lo[i])), mz = fmaxf(mz, fabsf(hi[i]));
 #pragma unroll
@@ -79,14 +99,30 @@ struct Row {
     }
     sa = store_dev::group_scale(ma, 127.f), sz = store_dev::group_scale(mz, 127.f);
   }
-  // Codes under those scales: four bytes a word, lower half then upper half.
-  __device__ __forceinline__ void codes(float fa, float fz, uint32_t (&ca)[2], uint32_t (&cz)[2]) const {
-    ca[0] = ca[1] = cz[0] = cz[1] = 0;
+  // Codes under those scales, rint(x / scale): four bytes a word, lower half then upper half.  x / scale is
+  // taken as x times the scale's reciprocal, within 127 x 2^-22 of the rounded quotient: the same integer
+  // unless it lies that near a half.  Where one of the eight does, or is no number, or passes 127 (a scale
+  // at fp16's end), all are divided.  Adding 1.5 x 2^23 rounds to an integer and leaves it in the low byte.
+  static __device__ __forceinline__ void codes8(const float (&x)[8], float f, float most, uint32_t (&c)[2]) {
+    const float r = f == 0.f ? 0.f : __frcp_rn(f), magic = 12582912.f;  // scale 0: codes 0
+    uint32_t far = most * r < 127.49f ? 0u : 0x7fffffffu, b[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      ca[i / 4] |= (store_dev::quant_code(lo[i], fa, 127) & 255) << (8 * (i % 4));
-      cz[i / 4] |= (store_dev::quant_code(hi[i], fz, 127) & 255) << (8 * (i % 4));
+      const float q = x[i] * r, t = q + magic, d = q - (t - magic);
+      b[i] = __float_as_uint(t);
+      far = max(far, __float_as_uint(d) & 0x7fffffffu);  // NaN's bits are above every number's
     }
+    c[0] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    c[1] = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    if (far > __float_as_uint(0.4999f)) {
+      c[0] = c[1] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i / 4] |= (store_dev::quant_code(x[i], f, 127) & 255) << (8 * (i % 4));
+    }
+  }
+  __device__ __forceinline__ void codes(float fa, float fz, uint32_t (&ca)[2], uint32_t (&cz)[2]) const {
+    codes8(lo, fa, ma, ca);
+    codes8(hi, fz, mz, cz);
   }
   __device__ __forceinline__ void from_codes(float fa, float fz, const uint2 a, const uint2 z) {
     const uint32_t ca[2] = {a.x, a.y}, cz[2] = {z.x, z.y};
@@ -112,25 +148,27 @@ __device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, in
   const KvPool& P = p.pool;
   const uint8_t* tile = page + P.off_heads + (long long)g * P.head_bytes;
   const __half* sc = reinterpret_cast<const __half*>(tile + (FMT == STARKV_KV_INT8 ? P.off_ks : 0));
-  float mn[16], mx[16];
+  uint32_t mn[8], mx[8];  // pairs of channels: lower half, upper half
 #pragma unroll
-  for (int i = 0; i < 16; ++i) mn[i] = __int_as_float(0x7f800000), mx[i] = __int_as_float(0xff800000);
+  for (int i = 0; i < 8; ++i) mn[i] = kPairInf<FMT>, mx[i] = kPairInf<FMT> | 0x80008000u;
 #pragma unroll
   for (int r1 = 0; r1 < kPage; r1 += 8) {
     const int r = r0 + r1, m = map[r];
-    Row<FMT> x;
+    Raw raw;
     if (FMT != STARKV_KV_INT8) {
-      const uint16_t* src = m < 0 ? reinterpret_cast<const uint16_t*>(tile) + r * D : p.k + m * p.k_stride + g * D;
-      x.set(load_raw<D>(src, j));
+      raw = load_raw<D>(m < 0 ? reinterpret_cast<const uint16_t*>(tile) + r * D : p.k + m * p.k_stride + g * D, j);
       if (m >= 0) {
+        Row<FMT> x;
         float2 c[8];
+        x.set(raw);
         angles<D>(p.rope, p.tok_pos[m], j, c);
         x.rotate(c);
-        x.set(x.rounded());
+        raw = x.rounded();
       }
     } else {
-      float2 c[8];
+      Row<FMT> x;
       if (m >= 0) {
+        float2 c[8];
         x.set(load_raw<D>(p.k + m * p.k_stride + g * D, j));
         angles<D>(p.rope, p.tok_pos[m], j, c);
         x.rotate(c);
@@ -146,36 +184,37 @@ __device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, in
         x.codes(__half2float(sa), __half2float(sz), ca, cz);
         x.from_codes(__half2float(sa), __half2float(sz), make_uint2(ca[0], ca[1]), make_uint2(cz[0], cz[1]));
       }
+      raw = x.rounded();
     }
+    const uint32_t w[8] = {raw.lo.x, raw.lo.y, raw.lo.z, raw.lo.w, raw.hi.x, raw.hi.y, raw.hi.z, raw.hi.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mn[i] = fminf(mn[i], x.lo[i]), mx[i] = fmaxf(mx[i], x.lo[i]);
-      mn[8 + i] = fminf(mn[8 + i], x.hi[i]), mx[8 + i] = fmaxf(mx[8 + i], x.hi[i]);
-    }
+    for (int i = 0; i < 8; ++i) mn[i] = pair_min<FMT>(mn[i], w[i]), mx[i] = pair_max<FMT>(mx[i], w[i]);
   }
 #pragma unroll
   for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      mn[i] = fminf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+    for (int i = 0; i < 8; ++i) {
+      mn[i] = pair_min<FMT>(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
+      mx[i] = pair_max<FMT>(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
     }
   if (r0 == 0) {
     uint16_t* dst = reinterpret_cast<uint16_t*>(page) + (long long)g * 2 * D + 8 * j;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // lower bounds of both halves, then upper
-      const float* v = (k < 2 ? mn : mx) + 8 * (k % 2);
-      *reinterpret_cast<uint4*>(dst + k * (D / 2)) =
-          make_uint4(kv_pack<FMT>(v[0], v[1]), kv_pack<FMT>(v[2], v[3]), kv_pack<FMT>(v[4], v[5]), kv_pack<FMT>(v[6], v[7]));
+      const uint32_t* v = (k < 2 ? mn : mx) + 4 * (k % 2);
+      *reinterpret_cast<uint4*>(dst + k * (D / 2)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   }
 }
 
-// One warp per task of kTask rows of a token (`slices` tasks a token); behind them, with BOUNDS, D / 64
-// warps per (token, KV head) that do something where the token completes its page.
-template <int FMT, int D, bool BOUNDS>
-__global__ void __launch_bounds__(32 * kAppendWarps, BOUNDS ? 2 : 4) kv_append_kernel(const KvAppendParams p, int slices) {
+// One warp per task of ROUNDS rounds of a token's rows, their loads in flight together (`slices` tasks a
+// token); behind them, with BOUNDS, D / 64 warps per (token, KV head) that do something where the token
+// completes its page.
+template <int FMT, int D, bool BOUNDS, int ROUNDS>
+__global__ void __launch_bounds__(32 * kAppendWarps, ROUNDS > 4 || BOUNDS ? 2 : ROUNDS > 2 ? 3 : 4)
+    kv_append_kernel(const KvAppendParams p, int slices) {
   using R = RowMap<D>;
+  constexpr int kTask = R::kRows * ROUNDS;
   __shared__ short s_map[BOUNDS ? kAppendWarps : 1][kPage];
   const KvPool& P = p.pool;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -206,10 +245,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, BOUNDS ? 2 : 4) kv_append_k
   }
   const int n = static_cast<int>(task / slices), slice = static_cast<int>(task % slices);
   const int j = lane % R::kLanes;
-  const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv, first = slice * R::kTask + lane / R::kLanes;
-  Raw raw[kRounds];
+  const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv, first = slice * kTask + lane / R::kLanes;
+  Raw raw[ROUNDS];
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
+  for (int i = 0; i < ROUNDS; ++i) {
     const int r = first + i * R::kRows;
     raw[i].lo = raw[i].hi = make_uint4(0, 0, 0, 0);
     if (r < rows) {
@@ -229,9 +268,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, BOUNDS ? 2 : 4) kv_append_k
   for (int i = 0; i < 8; ++i) c[i] = make_float2(0.f, 0.f);
   if (pos_ok) angles<D>(p.rope, pos, j, c);
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
+  for (int i = 0; i < ROUNDS; ++i) {
     const int r = first + i * R::kRows;
-    if (slice * R::kTask + i * R::kRows >= rows) break;  // the same for the whole warp
+    if (slice * kTask + i * R::kRows >= rows) break;  // the same for the whole warp
     const bool in = r < rows;
     const int kind = r < nq ? 0 : (r < nq + P.Hkv ? 1 : 2);
     const int h = kind == 0 ? r : (kind == 1 ? r - nq : r - nq - P.Hkv);
@@ -249,7 +288,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, BOUNDS ? 2 : 4) kv_append_k
       *reinterpret_cast<uint4*>(dst + 8 * j) = o.lo;
       *reinterpret_cast<uint4*>(dst + D / 2 + 8 * j) = o.hi;
     }
-    if (FMT == STARKV_KV_INT8 && slice * R::kTask + (i + 1) * R::kRows > nq) {  // not a round of queries alone
+    if (FMT == STARKV_KV_INT8 && slice * kTask + (i + 1) * R::kRows > nq) {  // not a round of queries alone
       __half sa, sz;
       x.scales(sa, sz);  // the whole warp shuffles
       if (in && kind != 0 && page) {
@@ -277,7 +316,7 @@ __global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p) 
   constexpr int CPR = D / CH, RPW = 32 / CPR;         // loads per row, rows per warp and load
   __shared__ int hit[kPage];
   __shared__ int hits;
-  __shared__ float s_mn[8][D], s_mx[8][D];
+  __shared__ uint4 s_mn[8][D / 8], s_mx[8][D / 8];  // per warp, eight channels an entry
   const KvPool& P = p.pool;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = blockIdx.y;
   pdl_wait();
@@ -296,52 +335,50 @@ __global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p) 
     if (!page) continue;  // the same for the whole CTA
     const uint8_t* tile = page + P.off_heads + (long long)g * P.head_bytes;
     const int ck = lane % CPR, r0 = 8 * warp + lane / CPR;
-    float lo[CH], hi[CH];
+    uint32_t lo[CH / 2], hi[CH / 2];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) lo[i] = __int_as_float(0x7f800000), hi[i] = __int_as_float(0xff800000);
+    for (int i = 0; i < CH / 2; ++i) lo[i] = kPairInf<FMT>, hi[i] = kPairInf<FMT> | 0x80008000u;
     const uint4* src = reinterpret_cast<const uint4*>(tile);
     const __half* sc = reinterpret_cast<const __half*>(tile + (FMT == STARKV_KV_INT8 ? P.off_ks : 0));
 #pragma unroll
     for (int r = 0; r < 8; r += RPW) {
       const uint4 x = src[(r0 + r) * CPR + ck];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t v[CH / 2];
       if (FMT == STARKV_KV_INT8) {
         const float s = __half2float(sc[(r0 + r) * (D / 32) + ck / 2]);
 #pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const float v = s * static_cast<float>(static_cast<int8_t>(w[i / 4] >> (8 * (i % 4))));
-          lo[i] = fminf(lo[i], v), hi[i] = fmaxf(hi[i], v);
-        }
+        for (int i = 0; i < CH / 2; ++i)
+          v[i] = kv_pack<FMT>(s * static_cast<float>(static_cast<int8_t>(w[i / 2] >> (16 * (i % 2)))),
+                              s * static_cast<float>(static_cast<int8_t>(w[i / 2] >> (16 * (i % 2) + 8))));
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = kv_unpack<FMT>(w[i]);
-          lo[2 * i] = fminf(lo[2 * i], v.x), hi[2 * i] = fmaxf(hi[2 * i], v.x);
-          lo[2 * i + 1] = fminf(lo[2 * i + 1], v.y), hi[2 * i + 1] = fmaxf(hi[2 * i + 1], v.y);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = w[i];
       }
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i) lo[i] = pair_min<FMT>(lo[i], v[i]), hi[i] = pair_max<FMT>(hi[i], v[i]);
     }
 #pragma unroll
     for (int o = CPR; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      for (int i = 0; i < CH / 2; ++i) {
+        lo[i] = pair_min<FMT>(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+        hi[i] = pair_max<FMT>(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
       }
     if (lane < CPR)
 #pragma unroll
-      for (int i = 0; i < CH; ++i) s_mn[warp][ck * CH + i] = lo[i], s_mx[warp][ck * CH + i] = hi[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      const int c = threadIdx.x % (D / 2) * 2;  // a pair of channels; the lower bounds, then the upper
-      const bool up = threadIdx.x >= D / 2;
-      float a = up ? s_mx[0][c] : s_mn[0][c], z = up ? s_mx[0][c + 1] : s_mn[0][c + 1];
-#pragma unroll
-      for (int w = 1; w < 8; ++w) {
-        a = up ? fmaxf(a, s_mx[w][c]) : fminf(a, s_mn[w][c]);
-        z = up ? fmaxf(z, s_mx[w][c + 1]) : fminf(z, s_mn[w][c + 1]);
+      for (int i = 0; i < CH / 8; ++i) {
+        s_mn[warp][ck * (CH / 8) + i] = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        s_mx[warp][ck * (CH / 8) + i] = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
       }
-      reinterpret_cast<uint32_t*>(page + (long long)g * 4 * D)[threadIdx.x] = kv_pack<FMT>(a, z);
+    __syncthreads();
+    if (threadIdx.x < D) {  // a pair of channels: the lower bounds, then the upper
+      const bool up = threadIdx.x >= D / 2;
+      const uint32_t* v = reinterpret_cast<const uint32_t*>(up ? s_mx[0] : s_mn[0]) + threadIdx.x % (D / 2);
+      uint32_t a = v[0];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) a = up ? pair_max<FMT>(a, v[w * (D / 2)]) : pair_min<FMT>(a, v[w * (D / 2)]);
+      reinterpret_cast<uint32_t*>(page + (long long)g * 4 * D)[threadIdx.x] = a;
     }
     __syncthreads();
   }
@@ -389,17 +426,22 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(const KvGatherParams p) 
   }
 }
 
+template <int FMT, int D, bool BOUNDS, int ROUNDS>
+cudaError_t append_rounds(const KvAppendParams& p, cudaStream_t s) {
+  constexpr int kTask = RowMap<D>::kRows * ROUNDS;
+  const int rows = (p.q ? p.pool.H : 0) + 2 * p.pool.Hkv, slices = (rows + kTask - 1) / kTask;
+  const long long tasks = (long long)p.n_tok * (slices + (BOUNDS ? p.pool.Hkv * (D / 64) : 0));
+  return launch_pdl(kv_append_kernel<FMT, D, BOUNDS, ROUNDS>,
+                    dim3(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)), dim3(32 * kAppendWarps), 0, s,
+                    p, slices);
+}
+
 template <int FMT, int D>
 cudaError_t append_launch(const KvAppendParams& p, cudaStream_t s) {
-  const int rows = (p.q ? p.pool.H : 0) + 2 * p.pool.Hkv;
-  const int slices = (rows + RowMap<D>::kTask - 1) / RowMap<D>::kTask;
   // Few tokens (decode steps, short prompts): the bounds in the same launch, where a completed page's
   // warp looks through the call's tokens.  Many: a launch behind it.
-  const bool fused = p.n_tok <= kFusedBoundsMax;
-  const long long tasks = (long long)p.n_tok * (slices + (fused ? p.pool.Hkv * (D / 64) : 0));
-  const dim3 grid(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)), block(32 * kAppendWarps);
-  if (fused) return launch_pdl(kv_append_kernel<FMT, D, true>, grid, block, 0, s, p, slices);
-  const cudaError_t e = launch_pdl(kv_append_kernel<FMT, D, false>, grid, block, 0, s, p, slices);
+  if (p.n_tok <= kFusedBoundsMax) return append_rounds<FMT, D, true, 2>(p, s);
+  const cudaError_t e = append_rounds<FMT, D, false, FMT == STARKV_KV_INT8 ? kRoundsInt8 : kRounds16>(p, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_bounds_kernel<FMT, D>, dim3((p.n_tok + kPage - 1) / kPage, p.pool.Hkv), dim3(256), 0, s, p);
 }
