@@ -657,24 +657,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvDecode
   const int G = p.pool.H / p.pool.Hkv, heads = p.pool.Hkv * p.groups;
   const int g = h / G, hv = g * p.groups + h % G / kKvRows, r = h % G % kKvRows;
   constexpr int per_page = Ring<FMT, D>::kParts;
+  // The lengths may be read before the wait: the split kernel, which does not write them, let this one
+  // start only after its own wait for all that came before.
+  const long long row = (long long)b * p.pool.H + h;
+  const int raw = p.seq_lens[b], count = span_of(p, b).count;
+  const List list = list_of(p, lane, per_page);
+  int before = 0;
+  for (int i = lane; i < b; i += 32) before += span_of(p, i).count;
+  before = __reduce_add_sync(0xffffffffu, before) * heads * per_page + hv * count * per_page;
+  // the chunks of this head's tiles
+  const int c0 = count ? list.chunk_of(before) : 0, c1 = count ? list.chunk_of(before + count * per_page - 1) : 0;
   pdl_wait();
   pdl_launch_dependents();
   if (threadIdx.x == 0 && h == 0 && b == 0) *p.counter = kTag;
-  const long long row = (long long)b * p.pool.H + h;
-  const int count = span_of(p, b).count;
-  if (threadIdx.x == 0 && h == 0 && (p.seq_lens[b] < 0 || p.seq_lens[b] > p.pool.max_pages * kPage))
-    atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+  if (threadIdx.x == 0 && h == 0 && (raw < 0 || raw > p.pool.max_pages * kPage)) atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
   if (count == 0) {
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(p.out + row * D)[threadIdx.x] = 0;
     if (p.lse && threadIdx.x == 0) p.lse[row] = __int_as_float(0xff800000);
     return;
   }
-  // the chunks of this head's tiles
-  const List list = list_of(p, lane, per_page);
-  int before = 0;
-  for (int i = lane; i < b; i += 32) before += span_of(p, i).count;
-  before = __reduce_add_sync(0xffffffffu, before) * heads * per_page + hv * count * per_page;
-  const int c0 = list.chunk_of(before), c1 = list.chunk_of(before + count * per_page - 1);
   if (c0 == c1) return;
   const long long rec0 = (long long)b * heads + hv;
   auto at = [&](int i) { return (rec0 + i) * p.rec_rows + r; };
