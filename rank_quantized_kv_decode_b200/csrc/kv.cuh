@@ -5,7 +5,9 @@
 namespace starkv {
 
 constexpr int kKvRows = 8;         // query heads of one KV head that a CTA takes together
-constexpr int kKvMaxCtas = 296;    // most CTAs of the split kernel: two on each of 148 SMs
+// CTAs of the split kernel on an SM (by its registers), and the most of a launch, on 148 SMs.
+constexpr int kv_split_ctas(int d) { return d == 64 ? 3 : 2; }
+constexpr int kv_max_ctas(int d) { return 148 * kv_split_ctas(d); }
 constexpr int kKvRounds = 8;       // small chunks per warp that a list is cut into, at most
 constexpr int kKvWarps = 4;        // warps of a split CTA
 

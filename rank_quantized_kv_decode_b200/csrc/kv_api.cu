@@ -59,7 +59,7 @@ int64_t kv_tiles(const starkv_kv_layout* lay, int64_t batch, int64_t max_pages) 
   return batch * lay->cfg.n_kv_heads * kv_groups(lay) * max_pages * (kPage / kv_tile_tokens(lay->cfg.fmt));
 }
 int64_t kv_pieces(const starkv_kv_layout* lay, int64_t batch) {
-  return static_cast<int64_t>(kKvMaxCtas) * kKvWarps * (1 + kKvRounds) + batch * lay->cfg.n_kv_heads * kv_groups(lay);
+  return static_cast<int64_t>(kv_max_ctas(lay->cfg.head_dim)) * kKvWarps * (1 + kKvRounds) + batch * lay->cfg.n_kv_heads * kv_groups(lay);
 }
 // Workspace: the counter, the sums, then (reference, sum) of the records.
 size_t kv_record_bytes(const starkv_kv_layout* lay, int64_t batch) {
@@ -344,9 +344,9 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   p.groups = kv_groups(lay);
   // as many CTAs as fit on the device, and no more than there can be pages
   const int64_t most = static_cast<int64_t>(batch) * p.pool.Hkv * p.groups * (sel && n_sel < max_pages ? n_sel : max_pages);
-  int64_t grid = 2 * static_cast<int64_t>(sms);
+  int64_t grid = static_cast<int64_t>(sms) * kv_split_ctas(p.pool.d);
   if (o.max_ctas > 0 && o.max_ctas < grid) grid = o.max_ctas;
-  if (grid > kKvMaxCtas) grid = kKvMaxCtas;
+  if (grid > kv_max_ctas(p.pool.d)) grid = kv_max_ctas(p.pool.d);
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
   p.counter = reinterpret_cast<unsigned long long*>(workspace);

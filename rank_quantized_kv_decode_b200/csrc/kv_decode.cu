@@ -50,13 +50,13 @@ template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   if (BF)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -65,24 +65,39 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 
 // fp16, upper rows only, onto zero.
 __device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a2, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, "
       "{%9,%9,%9,%9};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(0u), "r"(a2), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Loads from shared memory that stay in order with the waits (volatile) but, unlike with a memory clobber, let
+// everything else be scheduled around them.
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a)
-               : "memory");
+               : "r"(a));
 }
 
 // 16 bytes global -> shared; zeros when not `on` (the address is not read then).
@@ -108,8 +123,8 @@ struct Ring {
   static constexpr int kKeys = kTok * kRow;       // one tile's keys
   static constexpr int kScales = kInt8 ? kTok * (D / 32) * 2 : 0;
   static constexpr int kStage = 2 * kKeys + 2 * kScales;
-  static constexpr int kCtas = 2;  // per SM
-  static constexpr int kStages = kInt8 ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 6);
+  static constexpr int kCtas = kv_split_ctas(D);  // per SM
+  static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kBytes = kStage * kStages;
   static constexpr int kSmem = kKvWarps * kBytes;
 };
@@ -387,14 +402,14 @@ struct Sums {
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            const uint32_t w = ld_shared_u32(sc + (8 * h + 2 * t + i) * (D / 16) + 4 * j);
+            const uint32_t w = lds32(sc + (8 * h + 2 * t + i) * (D / 16) + 4 * j);
             const float2 x = kv_unpack<STARKV_KV_F16>(w);
             f[i][2 * j] = x.x, f[i][2 * j + 1] = x.y;
           }
         const int row = g + 8 * h;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint2 w = ld_shared_v2(stage + chunk_at<true, D>(row, 2 * j) + 8 * t);
+          const uint2 w = lds64(stage + chunk_at<true, D>(row, 2 * j) + 8 * t);
           uint32_t x[4];
           halves(w.x, x[0], x[1]);
           halves(w.y, x[2], x[3]);
@@ -489,10 +504,10 @@ struct Sums {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r0 = 2 * t + 8 * (h + e);
-            const uint2 x = ld_shared_v2(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
-            const uint2 y = ld_shared_v2(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
-            uint32_t f2 = ld_shared_u16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
-                          (uint32_t)ld_shared_u16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
+            const uint2 x = lds64(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
+            const uint2 y = lds64(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
+            uint32_t f2 = lds16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
+                          lds16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
             if (partial) {  // whatever the scales of rows that do not count hold
               if (r0 < lo || r0 >= hi) f2 &= 0xffff0000u;
               if (r0 + 1 < lo || r0 + 1 >= hi) f2 &= 0x0000ffffu;
@@ -728,7 +743,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvDecode
 template <int FMT, int D>
 cudaError_t decode_launch(const KvDecodeParams& p, cudaStream_t s) {
   using R = Ring<FMT, D>;
-  static_assert(R::kCtas == 2 && 2 * (R::kSmem + 2048) <= 228 * 1024, "two CTAs share an SM's memory");
+  static_assert(R::kCtas * (R::kSmem + 2048) <= 228 * 1024, "the CTAs of an SM share its memory");
   cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), R::kSmem, s, p);

@@ -44,12 +44,12 @@ def test_alloc_sizes(lib):
     assert s.cache_bytes == 7 * lay.page_bytes
     # the table of the latent cache at the same head_dim and length
     assert s.rope_table_bytes == (128 + 35) * 64 * 8
-    # a record of four heads for each piece: nine chunks for each of 296 x 4 warps, and one more where
+    # a record of four heads for each piece: nine chunks for each of 296 x 4 warps (d 64: 444 x 4), and one more where
     # each of 3 x 2 (sequence, KV head) ends; a counter before them
     assert s.decode_workspace_bytes == 256 + (296 * 4 * 9 + 3 * 2) * 4 * (128 * 4 + 8)
     # twenty query heads per KV head: three groups of at most eight
     s = api.kv_alloc(layout("bf16", 40, 2, 64), 1, 5, 32)
-    assert s.decode_workspace_bytes == 256 + (296 * 4 * 9 + 5 * 2 * 3) * 8 * (64 * 4 + 8)
+    assert s.decode_workspace_bytes == 256 + (444 * 4 * 9 + 5 * 2 * 3) * 8 * (64 * 4 + 8)
     for args in ((-1, 1, 1), (1, 1, 0), (1, 1, (1 << 24) + 1), (1 << 62, 1, 1), (1, -1, 1), (1, 65536, 1),
                  (1, 65535, 1 << 13)):
         with pytest.raises(L.StarkvError) as e:
