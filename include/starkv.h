@@ -526,7 +526,7 @@ STARKV_API starkv_status starkv_kv_select(const starkv_kv_layout* lay, const voi
 
 /* Settings of starkv_kv_decode (NULL = defaults). */
 typedef struct {
-  float scale;      /* of the scores; 0 = 1 / sqrt(d)                                        */
+  float scale;      /* of the scores, at most 1e38; 0 = 1 / sqrt(d)                          */
   int32_t window;   /* attend the last `window` tokens only; 0 = all                         */
   int32_t max_ctas; /* CTAs of the split kernel; 0 = as many as fit on the device            */
   int32_t reserved; /* 0                                                                     */

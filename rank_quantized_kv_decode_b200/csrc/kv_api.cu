@@ -313,7 +313,7 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   const starkv_kv_decode_opts none = {};
   const starkv_kv_decode_opts& o = opts ? *opts : none;
   if (batch < 0 || batch > kKvMaxBatch) return fail(STARKV_ERR_INVALID_ARG, "batch outside [0, 65535]");
-  if (!(o.scale >= 0.f) || !std::isfinite(o.scale)) return fail(STARKV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  if (!(o.scale >= 0.f) || o.scale > 1e38f) return fail(STARKV_ERR_INVALID_ARG, "scale must lie in [0, 1e38]");
   if (o.window < 0 || o.max_ctas < 0 || o.reserved != 0)
     return fail(STARKV_ERR_INVALID_ARG, "window or max_ctas < 0, or reserved not 0");
   if (sel && n_sel < 1) return fail(STARKV_ERR_INVALID_ARG, "n_sel < 1");

@@ -249,6 +249,47 @@ def test_token_by_token_and_read_back_equal_one_call(fmt):
         assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
+def test_one_launch_and_two_leave_the_same_pages(fmt):
+    # 256 tokens are stored and bounded in one launch, 257 in two; and in calls of 100
+    cs = [Case(fmt, 4, 2, 128, [400], seed=5) for _ in range(3)]
+    k, v = cs[0].draw(400, 2), cs[0].draw(400, 2)
+    for c, cut in zip(cs, ([0, 400], [0, 256, 400], [0, 100, 200, 300, 400])):
+        for a, b in zip(cut, cut[1:]):
+            c.append(k[a:b], v[a:b], np.zeros(b - a), np.arange(a, b))
+    assert np.array_equal(cs[0].pages(), cs[1].pages()) and np.array_equal(cs[0].pages(), cs[2].pages())
+
+
+def test_int8_codes_at_the_edges():
+    """Values stored as they are: quotients at and next to a half, groups of zeros, of subnormals, of one
+    large value, beyond fp16's largest scale, and an infinity; codes and scales are those of the oracle."""
+    c = Case("int8", 1, 1, 64, [300], seed=3)
+    r = c.rng
+    x = r.standard_normal((300, 64)).astype(np.float32)
+    # scale 1: the largest is 127, the others whole numbers and halves (ties to even)
+    x[:100] = r.integers(-254, 255, (100, 64)) / 2
+    x[:100, ::32] = 127
+    # other scales: the largest sets it, the others are halves of it before their rounding to bf16
+    for i in range(100, 200):
+        s = np.float32(np.float16(2.0 ** r.uniform(-20, 8)))
+        x[i] = (r.integers(-126, 127, 64) + 0.5) * s
+        x[i, ::32] = 127 * s
+    x[200] = 0
+    x[201, :32], x[201, 32:] = 0, 1e-8
+    x[202] = 1e-38
+    x[203], x[203, 5] = 1e-3, 3e4
+    x[204], x[204, 7] = 1e6, -3e38
+    x[205, 9] = np.inf
+    v = torch.from_numpy(x)[:, None].bfloat16().cuda()
+    c.append(v, v, np.zeros(300), np.arange(300))
+    _, codes, _, scales = K.read_raw(c.pages(), c.olay)
+    with np.errstate(over="ignore"):
+        wc, ws = K.quantise(f64(v))
+    page, slot = c.table_np[0][np.arange(300) // 64], np.arange(300) % 64
+    assert np.array_equal(scales[page, :, slot], ws)
+    assert np.array_equal(codes[page, :, slot], wc)
+
+
 def test_rewriting_slot_63_renews_the_bounds():
     c = Case("bf16", 2, 1, 64, [64])
     c.fill()
@@ -507,6 +548,44 @@ def test_equal_pages_are_chosen_from_the_lowest(pages):
     sel = c.select(q, n_sel, 0, 1).cpu().numpy()[0, 0]
     want = sorted(set(range(pages - 2)) | {pages // 2, pages - 1})
     assert list(sel) == want
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_select_with_numbers_that_are_none_still_gives_pages(what):
+    c = Case("bf16", 4, 2, 64, [64 * 40], seed=2)
+    c.fill()
+    k = c.k[:5].clone()
+    k[:, :, 3] = what
+    for i in range(5):  # pages 0, 7, ... with slot 63 again
+        p = 64 * 7 * i
+        c.append(torch.cat((k[i:i + 1], c.k[p + 63:p + 64])), torch.cat((c.v[:1], c.v[:1])), [0, 0], [p + 5, p + 63])
+    for q in (c.draw(1, 4), torch.full((1, 4, 64), what, dtype=torch.bfloat16, device="cuda")):
+        for n_sel in (2, 9, 39):
+            sel = c.select(q, n_sel, 1, 1).cpu().numpy()[0]
+            for g in range(2):
+                assert np.all(np.diff(sel[g]) > 0) and sel[g, 0] == 0 and sel[g, -1] == 39
+    assert c.status() == 0
+
+
+@pytest.mark.parametrize("n_sel,first,last", [(50, 1, 2), (1000, 0, 1), (16383, 2, 3)])
+def test_select_over_the_longest_table_with_many_equal_pages(n_sel, first, last):
+    """A million tokens: 16384 places that share 90 pages, so that every score stands many times and the
+    border falls among equal ones; then attention over the choice."""
+    pages = 16384
+    c = Case("bf16", 4, 1, 64, [64 * 90], seed=21)
+    c.fill()
+    order = np.concatenate([c.table_np[0], c.table_np[0][c.rng.integers(0, 90, pages - 90)]])
+    c.table_np = order[None].astype(np.int32)
+    c.table = torch.from_numpy(c.table_np).cuda()
+    c.lens = [pages * 64 - 13]
+    c.len_t = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    q = c.draw(1, 4, 1.5)
+    sel = c.select(q, n_sel, first, last).cpu().numpy()
+    s = K.page_scores(f64(q)[0], K.read_bounds(c.pages(), c.olay)[c.table_np[0]])
+    assert np.array_equal(sel[0, 0], K.choose(s[0], c.lens[0], n_sel, first, last))
+    assert c.status() == 0
+    out, lse = c.decode(q, sel=torch.from_numpy(sel).int().cuda())
+    c.check(q, out, lse, sel=sel)
 
 
 def test_select_flags_a_bad_page_and_ranks_it_last():

@@ -2,6 +2,9 @@
 layout, refusals of the entry points and of the binding before anything touches a device, and
 the oracle's pieces on cases worked out by hand."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -129,7 +132,7 @@ def decode(lib, lay, q=P16, cache=P16, pages=1, bt=P16, mp=2, lens=P16, batch=1,
     (dict(out=ODD), L.ERR_INVALID_ARG), (dict(cache=ODD), L.ERR_INVALID_ARG), (dict(ws=ODD), L.ERR_INVALID_ARG),
     (dict(sel=P16, n_sel=0), L.ERR_INVALID_ARG), (dict(sel=P16, n_sel=4, opts=(0.0, 64, 0, 0)), L.ERR_INVALID_ARG),
     (dict(opts=(-1.0, 0, 0, 0)), L.ERR_INVALID_ARG), (dict(opts=(float("nan"), 0, 0, 0)), L.ERR_INVALID_ARG),
-    (dict(opts=(float("inf"), 0, 0, 0)), L.ERR_INVALID_ARG), (dict(opts=(0.0, -1, 0, 0)), L.ERR_INVALID_ARG),
+    (dict(opts=(float("inf"), 0, 0, 0)), L.ERR_INVALID_ARG), (dict(opts=(3e38, 0, 0, 0)), L.ERR_INVALID_ARG), (dict(opts=(0.0, -1, 0, 0)), L.ERR_INVALID_ARG),
     (dict(opts=(0.0, 0, -1, 0)), L.ERR_INVALID_ARG), (dict(opts=(0.0, 0, 0, 1)), L.ERR_INVALID_ARG),
     (dict(wb=64), L.ERR_WORKSPACE)])
 def test_decode_refuses_before_touching_the_device(lib, kw, status):
@@ -225,3 +228,50 @@ def test_oracle_attention_by_hand():
     v = np.array([[[1.0, 2, 3, 4], [3.0, 4, 5, 6]]])
     o, lse, _, _ = K.attention(np.ones((2, 4)), k, v)
     assert np.allclose(o, [[2, 3, 4, 5]] * 2) and np.allclose(lse, 2.0 + np.log(2.0))
+
+
+C_PROGRAM = r"""
+#include <stdio.h>
+#include <string.h>
+#include "starkv.h"
+
+int main(void) {
+  starkv_kv_config cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.n_q_heads = 32;
+  cfg.n_kv_heads = 8;
+  cfg.head_dim = 128;
+  cfg.fmt = STARKV_KV_INT8;
+  cfg.page_tokens = 64;
+  cfg.rope_theta = 500000.0;
+  starkv_kv_layout lay;
+  starkv_kv_sizes sz;
+  if (starkv_kv_layout_init(&cfg, &lay) != STARKV_OK) return 1;
+  if (starkv_kv_alloc(&lay, 10, 4, 8, &sz) != STARKV_OK) return 2;
+  /* refused before the device is touched */
+  if (starkv_kv_append(&lay, NULL, 0, NULL, 0, NULL, 0, -1, NULL, NULL, NULL, 1, 1, NULL, 0, NULL, 1, NULL, NULL,
+                       NULL) != STARKV_ERR_INVALID_ARG) return 3;
+  if (starkv_kv_gather(&lay, NULL, 1, NULL, NULL, 0, NULL, 1, 1, NULL, NULL, NULL, NULL) != STARKV_OK) return 4;
+  if (starkv_kv_select(&lay, NULL, NULL, 1, NULL, 1, NULL, 1, 4, 0, 0, NULL, NULL, NULL) != STARKV_ERR_INVALID_ARG) return 5;
+  if (starkv_kv_decode(&lay, NULL, NULL, 1, NULL, 1, NULL, 0, NULL, 0, NULL, NULL, NULL, NULL, 0, NULL, NULL) !=
+      STARKV_OK) return 6;
+  printf("%lld %lld %lld\n", (long long)lay.page_bytes, (long long)lay.off_ks, (long long)sz.cache_bytes);
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler")
+def test_c99_caller(lib, tmp_path):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    libdir = os.path.join(root, "rank_quantized_kv_decode_b200")
+    src, exe = tmp_path / "caller.c", tmp_path / "caller"
+    src.write_text(C_PROGRAM)
+    proc = subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o",
+                           str(exe), "-L", libdir, "-lstarkv", "-Wl,-rpath," + libdir,
+                           "-Wl,--unresolved-symbols=ignore-in-shared-libs"], capture_output=True, text=True)
+    assert proc.returncode == 0, proc.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, (run.returncode, run.stdout)
+    want = K.kv_page_layout("int8", 8, 128)
+    assert run.stdout.split() == [str(want["page_bytes"]), str(want["off_ks"]), str(10 * want["page_bytes"])]
