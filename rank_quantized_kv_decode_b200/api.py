@@ -332,136 +332,142 @@ def kv_rope_init(lay: L.KvLayout, max_pages: int, table: torch.Tensor, stream=No
             "starkv_kv_rope_init")
 
 
-# The checks below are those of _need and _ptr, ordered for a short way through: a decode step makes
-# several of these calls per layer and its kernels run for a few microseconds.
-def _kv_device(t) -> int:
-    """Device index of a call's cache, which has to be the current one."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("expected a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    return dev
-
-
-def _kv_ptr(t, dev: int) -> int | None:
+# The checks below are those of _need and _ptr in one pass per argument, for a short way through: a decode
+# step makes several of these calls per layer and its kernels run for a few microseconds.  Arguments are
+# held against the cache's device, and that, at the end, against the current one.
+def _kv_arg(t, name: str, dtype, least: int, dev: int) -> int | None:
+    """Pointer of a contiguous argument of ``dtype`` with at least ``least`` elements on ``dev``."""
     if t is None:
         return None
+    if t.dtype is not dtype or t.numel() < least:
+        _need(t, name, dtype, least)
     if t.get_device() != dev:
         raise ValueError("expected a CUDA tensor" if t.get_device() < 0 else
-                         f"tensor on {t.device}, but the current device is cuda:{dev}")
+                         f"{name}: tensor on {t.device}, but the cache is on cuda:{dev}")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
     return t.data_ptr()
 
 
-def _kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int) -> int:
-    """Token stride of [n_tok][heads][d]; a token's heads are contiguous, the tokens may be slices of
-    wider rows."""
-    if t.dtype != dtype:
+def _kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int, dev: int) -> tuple[int | None, int]:
+    """Pointer and token stride of [n_tok][heads][d]; a token's heads are contiguous, the tokens may be
+    slices of wider rows."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
     shape, strides = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != d or shape[0] < n_tok:
         raise ValueError(f"{name}: expected shape ({n_tok}, {heads}, {d}), got {tuple(shape)}")
     if strides[2] != 1 or (heads > 1 and strides[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {strides}")
-    return strides[0] if shape[0] > 1 else heads * d
-
-
-def _kv_row_ptr(t, dev: int) -> int:
     if t.get_device() != dev:
-        return _kv_ptr(t, dev)  # raises
-    return t.data_ptr()
+        raise ValueError("expected a CUDA tensor" if t.get_device() < 0 else
+                         f"{name}: tensor on {t.device}, but the cache is on cuda:{dev}")
+    return t.data_ptr(), strides[0] if shape[0] > 1 else heads * d
 
 
-def _check_kv_batch(lay, q, block_table, seq_lens, status) -> tuple[int, int]:
-    """(batch, row length of the block table)."""
-    c = lay.cfg
-    _need(seq_lens, "seq_lens", torch.int32, ndim=1)
-    _need(block_table, "block_table", torch.int32, ndim=2)
-    batch, (rows, width) = seq_lens.shape[0], block_table.shape
-    if rows < batch:
-        raise ValueError(f"block_table: {rows} rows for {batch} sequences")
-    _need(q, "q", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim)
-    _need(status, "status", torch.int32, 1)
-    return batch, width
+def _kv_table(block_table, batch: int, dev: int) -> tuple[int, int, int]:
+    """(pointer, rows, row length) of a block table with at least ``batch`` rows."""
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"block_table: expected 2 dimensions, got shape {tuple(shape)}")
+    if shape[0] < batch:
+        raise ValueError(f"block_table: {shape[0]} rows for {batch} sequences")
+    return _kv_arg(block_table, "block_table", torch.int32, 0, dev), shape[0], shape[1]
 
 
-def _check_kv_sel(lay, sel, batch: int) -> int:
-    _need(sel, "sel", torch.int32, ndim=3)
-    rows, heads, n_sel = sel.shape
-    if rows < batch or heads != lay.cfg.n_kv_heads:
-        raise ValueError(f"sel: expected ({batch}, {lay.cfg.n_kv_heads}, pages), got {tuple(sel.shape)}")
-    return n_sel
+def _kv_stream(dev: int, stream) -> int:
+    """Stream handle, once the arguments' device is found to be the current one."""
+    if dev < 0:
+        raise ValueError("expected a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"cache on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _kv_sel(lay, sel, batch: int, dev: int) -> tuple[int, int]:
+    """(pointer, pages) of a selection [batch][H_kv][pages]."""
+    shape = sel.shape
+    if len(shape) != 3:
+        raise ValueError(f"sel: expected 3 dimensions, got shape {tuple(shape)}")
+    if shape[0] < batch or shape[1] != lay.cfg.n_kv_heads:
+        raise ValueError(f"sel: expected ({batch}, {lay.cfg.n_kv_heads}, pages), got {tuple(shape)}")
+    return _kv_arg(sel, "sel", torch.int32, 0, dev), shape[2]
+
+
+def _kv_lens(seq_lens, dev: int) -> tuple[int, int]:
+    """(pointer, sequences)."""
+    if seq_lens.dim() != 1:
+        raise ValueError(f"seq_lens: expected 1 dimensions, got shape {tuple(seq_lens.shape)}")
+    return _kv_arg(seq_lens, "seq_lens", torch.int32, 0, dev), seq_lens.numel()
 
 
 def kv_append(lay, k, v, tok_seq, tok_pos, block_table, cache, rope_table, status, q=None, q_out=None,
               stream=None) -> None:
     """Rotate and store keys and values [n][H_kv][d] of new tokens (slices of a fused projection
     will do), update the bounds of the pages they complete, and rotate their queries into q_out."""
-    c = lay.cfg
+    c, dev = lay.cfg, cache.get_device()
     dt, n_tok, H, Hkv, d = _KV_DTYPE[c.fmt], k.shape[0], c.n_q_heads, c.n_kv_heads, c.head_dim
-    _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
-    _need(q_out, "q_out", dt, n_tok * H * d)
-    qs = _kv_rows(q, "q", dt, n_tok, H, d) if q is not None else 0
-    ks, vs = _kv_rows(k, "k", dt, n_tok, Hkv, d), _kv_rows(v, "v", dt, n_tok, Hkv, d)
-    dev = _kv_device(cache)
-    rows, width = block_table.shape
+    kp, ks = _kv_rows(k, "k", dt, n_tok, Hkv, d, dev)
+    vp, vs = _kv_rows(v, "v", dt, n_tok, Hkv, d, dev)
+    qp, qs = _kv_rows(q, "q", dt, n_tok, H, d, dev)
+    table, rows, width = _kv_table(block_table, 0, dev)
     L.check(L.load().starkv_kv_append(
-        ctypes.byref(lay), _kv_row_ptr(q, dev) if q is not None else None, qs, _kv_row_ptr(k, dev), ks,
-        _kv_row_ptr(v, dev), vs, n_tok, _kv_ptr(tok_seq, dev), _kv_ptr(tok_pos, dev),
-        _kv_ptr(block_table, dev), width, rows, _kv_ptr(rope_table, dev), rope_table.nbytes,
-        _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes, _kv_ptr(q_out, dev), _kv_ptr(status, dev),
-        _stream(stream)), "starkv_kv_append")
+        ctypes.byref(lay), qp, qs, kp, ks, vp, vs, n_tok, _kv_arg(tok_seq, "tok_seq", torch.int32, n_tok, dev),
+        _kv_arg(tok_pos, "tok_pos", torch.int32, n_tok, dev), table, width, rows,
+        _kv_arg(rope_table, "rope_table", rope_table.dtype, 0, dev), rope_table.nbytes,
+        _kv_arg(cache, "cache", cache.dtype, 0, dev), cache.nbytes // lay.page_bytes,
+        _kv_arg(q_out, "q_out", dt, n_tok * H * d, dev), _kv_arg(status, "status", torch.int32, 1, dev),
+        _kv_stream(dev, stream)), "starkv_kv_append")
 
 
 def kv_gather(lay, cache, tok_seq, tok_pos, block_table, k_out, v_out, status, stream=None) -> None:
     """Stored keys (rotated) and values of tokens, [n][H_kv][d]."""
-    c = lay.cfg
-    n_tok = tok_seq.shape[0]
-    _check_tokens(n_tok, tok_seq, tok_pos, block_table, status)
-    _need(k_out, "k_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
-    _need(v_out, "v_out", _KV_DTYPE[c.fmt], n_tok * c.n_kv_heads * c.head_dim)
-    dev = _kv_device(cache)
-    rows, width = block_table.shape
+    c, dev = lay.cfg, cache.get_device()
+    dt, n_tok = _KV_DTYPE[c.fmt], tok_seq.shape[0]
+    size = n_tok * c.n_kv_heads * c.head_dim
+    table, rows, width = _kv_table(block_table, 0, dev)
     L.check(L.load().starkv_kv_gather(
-        ctypes.byref(lay), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes, _kv_ptr(tok_seq, dev),
-        _kv_ptr(tok_pos, dev), n_tok, _kv_ptr(block_table, dev), width, rows, _kv_ptr(k_out, dev),
-        _kv_ptr(v_out, dev), _kv_ptr(status, dev), _stream(stream)), "starkv_kv_gather")
+        ctypes.byref(lay), _kv_arg(cache, "cache", cache.dtype, 0, dev), cache.nbytes // lay.page_bytes,
+        _kv_arg(tok_seq, "tok_seq", torch.int32, n_tok, dev), _kv_arg(tok_pos, "tok_pos", torch.int32, n_tok, dev),
+        n_tok, table, width, rows, _kv_arg(k_out, "k_out", dt, size, dev), _kv_arg(v_out, "v_out", dt, size, dev),
+        _kv_arg(status, "status", torch.int32, 1, dev), _kv_stream(dev, stream)), "starkv_kv_gather")
 
 
 def kv_select(lay, q, cache, block_table, seq_lens, sel, status, keep_first: int = 0,
               keep_last: int = 1, stream=None) -> None:
     """Choose sel.shape[2] pages per sequence and KV head into sel [batch][H_kv][pages]."""
-    batch, width = _check_kv_batch(lay, q, block_table, seq_lens, status)
-    n_sel = _check_kv_sel(lay, sel, batch)
-    dev = _kv_device(cache)
+    c, dev = lay.cfg, cache.get_device()
+    lens, batch = _kv_lens(seq_lens, dev)
+    table, _, width = _kv_table(block_table, batch, dev)
+    sp, n_sel = _kv_sel(lay, sel, batch, dev)
     L.check(L.load().starkv_kv_select(
-        ctypes.byref(lay), _kv_ptr(q, dev), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes,
-        _kv_ptr(block_table, dev), width, _kv_ptr(seq_lens, dev), batch, n_sel, keep_first, keep_last,
-        _kv_ptr(sel, dev), _kv_ptr(status, dev), _stream(stream)), "starkv_kv_select")
+        ctypes.byref(lay), _kv_arg(q, "q", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim, dev),
+        _kv_arg(cache, "cache", cache.dtype, 0, dev), cache.nbytes // lay.page_bytes, table, width, lens, batch,
+        n_sel, keep_first, keep_last, sp, _kv_arg(status, "status", torch.int32, 1, dev),
+        _kv_stream(dev, stream)), "starkv_kv_select")
 
 
 def kv_decode(lay, q, cache, block_table, seq_lens, out, workspace, status, sel=None, lse=None,
               scale: float = 0.0, window: int = 0, max_ctas: int = 0, stream=None) -> None:
     """Attention of one (rotated) token per sequence over its cached tokens, or over the pages of
     ``sel``."""
-    c = lay.cfg
-    batch, width = _check_kv_batch(lay, q, block_table, seq_lens, status)
-    rows = batch * c.n_q_heads
-    _need(out, "out", _KV_DTYPE[c.fmt], rows * c.head_dim)
-    _need(lse, "lse", torch.float32, rows)
-    n_sel = _check_kv_sel(lay, sel, batch) if sel is not None else 0
+    c, dev = lay.cfg, cache.get_device()
+    lens, batch = _kv_lens(seq_lens, dev)
+    table, _, width = _kv_table(block_table, batch, dev)
+    dt, rows = _KV_DTYPE[c.fmt], batch * c.n_q_heads
+    size = rows * c.head_dim
+    sp, n_sel = _kv_sel(lay, sel, batch, dev) if sel is not None else (None, 0)
     opts = None
     if scale or window or max_ctas:
         opts = ctypes.byref(L.KvDecodeOpts(scale, window, max_ctas, 0))
-    dev = _kv_device(cache)
     L.check(L.load().starkv_kv_decode(
-        ctypes.byref(lay), _kv_ptr(q, dev), _kv_ptr(cache, dev), cache.nbytes // lay.page_bytes,
-        _kv_ptr(block_table, dev), width, _kv_ptr(seq_lens, dev), batch, _kv_ptr(sel, dev), n_sel, opts,
-        _kv_ptr(out, dev), _kv_ptr(lse, dev), _kv_ptr(workspace, dev), workspace.nbytes,
-        _kv_ptr(status, dev), _stream(stream)), "starkv_kv_decode")
+        ctypes.byref(lay), _kv_arg(q, "q", dt, size, dev), _kv_arg(cache, "cache", cache.dtype, 0, dev),
+        cache.nbytes // lay.page_bytes, table, width, lens, batch, sp, n_sel, opts,
+        _kv_arg(out, "out", dt, size, dev), _kv_arg(lse, "lse", torch.float32, rows, dev),
+        _kv_arg(workspace, "workspace", workspace.dtype, 0, dev), workspace.nbytes,
+        _kv_arg(status, "status", torch.int32, 1, dev), _kv_stream(dev, stream)), "starkv_kv_decode")
 
 
 def diag_bounded_wait(timeout_ms: int, status, stream=None) -> None:
