@@ -105,6 +105,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
   const int n = on ? 16 : 0;
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -127,6 +130,11 @@ struct Ring {
   static constexpr int kStages = D == 128 ? 3 : 4;
   static constexpr int kBytes = kStage * kStages;
   static constexpr int kSmem = kKvWarps * kBytes;
+  // What a chunk's place changes by (exclusive or) from row r, below `rows`, to row r + rows, beside the
+  // rows' pitch: chunk_at's permutation.
+  static __device__ constexpr uint32_t turn(int rows) {
+    return !kInt8 ? (rows & 7) << 4 : D == 128 ? (rows >> 1 & 2) << 5 : 0;
+  }
 };
 
 // Offset of a 16-byte chunk of a tile's row in shared memory: the chunks are permuted so that the
@@ -299,15 +307,28 @@ __device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Piece& c,
 template <int FMT, int D>
 __device__ __forceinline__ void load_tile(const KvDecodeParams& p, const Tile& t, uint32_t stage, int part, int lane) {
   using R = Ring<FMT, D>;
-  constexpr int CPR = R::kRow / 16, N = R::kTok * CPR;
-  const uint8_t* k = t.src + part * R::kKeys;
+  // round i takes chunk lane + 32 i: the row moves by 32 / CPR, the place in shared memory by 512 bytes and
+  // the permutation's change, known here
+  constexpr int CPR = R::kRow / 16, N = R::kTok * CPR / 32, step = 32 / CPR;
+  const uint8_t* k = t.src + part * R::kKeys + lane * 16;
   const uint8_t* v = k + p.pool.off_v;
+  const int row = lane / CPR;
+  const uint32_t to = stage + chunk_at<R::kInt8, D>(row, lane % CPR);
+  if (t.lo == 0 && t.hi == R::kTok) {
 #pragma unroll
-  for (int i = lane; i < N; i += 32) {
-    const int row = i / CPR, at = chunk_at<R::kInt8, D>(row, i % CPR);
-    const bool on = row >= t.lo && row < t.hi;
-    cp16(stage + at, k + i * 16, on);
-    cp16(stage + R::kKeys + at, v + i * 16, on);
+    for (int i = 0; i < N; ++i) {
+      const uint32_t at = (to ^ R::turn(i * step)) + 512 * i;
+      cp16(at, k + 512 * i);
+      cp16(at + R::kKeys, v + 512 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint32_t at = (to ^ R::turn(i * step)) + 512 * i;
+      const bool on = row + i * step >= t.lo && row + i * step < t.hi;
+      cp16(at, k + 512 * i, on);
+      cp16(at + R::kKeys, v + 512 * i, on);
+    }
   }
   if constexpr (R::kInt8) {
     constexpr int SC = R::kScales / 16;  // 16-byte chunks of a tile's scales (several tokens each)
@@ -378,14 +399,15 @@ struct Sums {
   __device__ __forceinline__ void scores(uint32_t stage, int lane, float (&s)[2 * kHalves]) const {
     using R = Ring<FMT, D>;
     if constexpr (!kInt8) {
-      const int mi = lane / 8, row = lane % 8 + 8 * (mi >> 1);
+      const int mi = lane / 8;
+      const uint32_t from = stage + chunk_at<false, D>(lane % 8 + 8 * (mi >> 1), mi & 1);
 #pragma unroll
       for (int h = 0; h < kHalves; h += 2) {
         float c[2][4] = {};
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t f[4];
-          ldsm4(f, stage + chunk_at<false, D>(8 * h + row, 2 * k + (mi & 1)));
+          ldsm4(f, (from ^ (k << 5)) + 8 * h * R::kRow);
           mma16816<kBf>(c[0], q[k][0], 0u, q[k][1], 0u, f[0], f[1]);
           mma16816<kBf>(c[1], q[k][0], 0u, q[k][1], 0u, f[2], f[3]);
         }
@@ -393,23 +415,30 @@ struct Sums {
       }
     } else {
       const int g = lane / 4, t = lane % 4;
-      const uint32_t sc = stage + 2 * R::kKeys;
+      const uint32_t from = stage + chunk_at<true, D>(g, 0) + 8 * t;
+      const uint32_t sc = stage + 2 * R::kKeys + 2 * t * (D / 16);
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         // the fp32 scales of this lane's two result columns
         float f[2][D / 32];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[2];
+          if constexpr (D == 128) {
+            const uint2 x = lds64(sc + (8 * h + i) * (D / 16));
+            w[0] = x.x, w[1] = x.y;
+          } else {
+            w[0] = lds32(sc + (8 * h + i) * (D / 16));
+          }
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            const uint32_t w = lds32(sc + (8 * h + 2 * t + i) * (D / 16) + 4 * j);
-            const float2 x = kv_unpack<STARKV_KV_F16>(w);
+            const float2 x = kv_unpack<STARKV_KV_F16>(w[j]);
             f[i][2 * j] = x.x, f[i][2 * j + 1] = x.y;
           }
-        const int row = g + 8 * h;
+        }
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
-          const uint2 w = lds64(stage + chunk_at<true, D>(row, 2 * j) + 8 * t);
+          const uint2 w = lds64((from ^ (j << 5)) + 8 * h * R::kRow);
           uint32_t x[4];
           halves(w.x, x[0], x[1]);
           halves(w.y, x[2], x[3]);
@@ -480,13 +509,14 @@ struct Sums {
     }
     const uint32_t vs = stage + R::kKeys;
     if constexpr (!kInt8) {
-      const int mi = lane / 8, row = lane % 8 + 8 * (mi & 1);
+      const int mi = lane / 8;
+      const uint32_t from = vs + chunk_at<false, D>(lane % 8 + 8 * (mi & 1), mi >> 1);
 #pragma unroll
       for (int h = 0; h < kHalves; h += 2)
 #pragma unroll
         for (int n = 0; n < D / 16; ++n) {
           uint32_t f[4];
-          ldsm4t(f, vs + chunk_at<false, D>(8 * h + row, 2 * n + (mi >> 1)));
+          ldsm4t(f, (from ^ (n << 5)) + 8 * h * R::kRow);
           mma16816<kBf>(o[2 * n], ah[h], al[h], ah[h + 1], al[h + 1], f[0], f[1]);
           mma16816<kBf>(o[2 * n + 1], ah[h], al[h], ah[h + 1], al[h + 1], f[2], f[3]);
         }
@@ -494,24 +524,29 @@ struct Sums {
       // Column n = lane / 4 of product (jj, i) is channel 8 (n + 8 jj) + i: a lane decodes eight
       // neighbouring channels of four tokens, code times scale rounded once to fp16.
       const int g = lane / 4;
-      const uint32_t sc = stage + 2 * R::kKeys + R::kScales;
+      uint32_t sc = stage + 2 * R::kKeys + R::kScales;
+      if (partial) {  // whatever the scales of rows that do not count hold
+        for (int i = lane; i < R::kScales / 4; i += 32) {
+          const int r = i / (D / 64);
+          if (r < lo || r >= hi) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sc + 4 * i), "r"(0u) : "memory");
+        }
+        __syncwarp();
+      }
+      sc += 2 * t * (D / 16) + 2 * (g >> 2);
+      // rows 2t and 2t + 1, unit g of eight channels
+      const uint32_t fx = vs + chunk_at<true, D>(2 * t, g >> 1) + 8 * (g & 1);
+      const uint32_t fy = vs + chunk_at<true, D>(2 * t + 1, g >> 1) + 8 * (g & 1);
 #pragma unroll
       for (int h = 0; h < kHalves; h += 2)
 #pragma unroll
         for (int jj = 0; jj < D / 64; ++jj) {
-          const int u = g + 8 * jj;
           uint32_t b[2][8];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int r0 = 2 * t + 8 * (h + e);
-            const uint2 x = lds64(vs + chunk_at<true, D>(r0, u >> 1) + 8 * (u & 1));
-            const uint2 y = lds64(vs + chunk_at<true, D>(r0 + 1, u >> 1) + 8 * (u & 1));
-            uint32_t f2 = lds16(sc + r0 * (D / 16) + 2 * (u >> 2)) |
-                          lds16(sc + (r0 + 1) * (D / 16) + 2 * (u >> 2)) << 16;
-            if (partial) {  // whatever the scales of rows that do not count hold
-              if (r0 < lo || r0 >= hi) f2 &= 0xffff0000u;
-              if (r0 + 1 < lo || r0 + 1 >= hi) f2 &= 0x0000ffffu;
-            }
+            const uint2 x = lds64((fx ^ (jj << 6)) + 8 * (h + e) * R::kRow);
+            const uint2 y = lds64((fy ^ (jj << 6)) + 8 * (h + e) * R::kRow);
+            const uint32_t at = sc + 8 * (h + e) * (D / 16) + 4 * jj;
+            const uint32_t f2 = __byte_perm(lds16(at), lds16(at + D / 16), 0x5410);
             const __half2 f = *reinterpret_cast<const __half2*>(&f2);
 #pragma unroll
             for (int w2 = 0; w2 < 2; ++w2) {
@@ -582,7 +617,7 @@ constexpr unsigned long long kTag = 0x73744b56ull << 32;
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_kernel(const KvDecodeParams p) {
   using R = Ring<FMT, D>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];  // the fragments' addresses are formed by exclusive or
   // what the tile in a stage of a warp's ring is: sequence, KV head, chunk, and [lo, hi) with flags
   __shared__ int4 s_what[kKvWarps][R::kStages];
   constexpr int kFirst = 1 << 16, kLast = 1 << 17, kWhole = 1 << 18, kThere = 1 << 19;
