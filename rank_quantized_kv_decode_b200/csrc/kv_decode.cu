@@ -282,26 +282,35 @@ __device__ __forceinline__ void next_piece(const KvDecodeParams& p, Piece& c, in
 }
 
 // ------------------------------------------------------------------ loads
+// The page that a warp is in: where the head's tile of it lies (null: none), and what counts of its 64
+// rows: [lo, hi).
+struct Page {
+  const uint8_t* src;
+  int lo, hi;
+};
+// Page i of the piece (whole warp).
+__device__ __forceinline__ Page page_of(const KvDecodeParams& p, const Piece& c, int i) {
+  Page t{nullptr, 0, 0};
+  const int page = __shfl_sync(0xffffffffu, c.page, i - c.page0), at = __shfl_sync(0xffffffffu, c.at, i - c.page0);
+  if (at < 0) return t;
+  if (page < 0 || page >= p.pool.num_pages) {
+    atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
+    return t;
+  }
+  t.src = p.pool.cache + page * p.pool.page_bytes + p.pool.off_heads + (long long)(c.hv / p.groups) * p.pool.head_bytes;
+  t.hi = min(max(c.s.len - at * kPage, 0), kPage);
+  t.lo = p.window > 0 ? min(max(c.s.len - p.window - at * kPage, 0), kPage) : 0;
+  return t;
+}
+
 // Where a tile lies, and which of its rows count: [lo, hi).
 struct Tile {
   const uint8_t* src;  // the head's tile of the page
   int lo, hi;
 };
 template <int TOK>
-__device__ __forceinline__ Tile tile_of(const KvDecodeParams& p, const Piece& c, int part) {
-  Tile t{nullptr, 0, 0};
-  const int i = c.tile / (kPage / TOK) - c.page0;
-  const int page = __shfl_sync(0xffffffffu, c.page, i), at = __shfl_sync(0xffffffffu, c.at, i);
-  if (at < 0) return t;
-  if (page < 0 || page >= p.pool.num_pages) {
-    atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
-    return t;
-  }
-  const int t0 = at * kPage + part * TOK;
-  t.src = p.pool.cache + page * p.pool.page_bytes + p.pool.off_heads + (long long)(c.hv / p.groups) * p.pool.head_bytes;
-  t.hi = min(max(c.s.len - t0, 0), TOK);
-  t.lo = p.window > 0 ? min(max(c.s.len - p.window - t0, 0), TOK) : 0;
-  return t;
+__device__ __forceinline__ Tile tile_of(const Page& g, int part) {
+  return {g.src, min(max(g.lo - part * TOK, 0), TOK), min(max(g.hi - part * TOK, 0), TOK)};
 }
 
 template <int FMT, int D>
@@ -567,38 +576,50 @@ struct Sums {
     }
   }
 
-  // The sums of the piece of (b, hv): the result where it is the whole sequence, else a record.
-  __device__ __forceinline__ void end(const KvDecodeParams& p, int b, int hv, bool whole, int chunk, int lane) {
+  // The sums of the piece of (b, hv): the result where it is the whole sequence, else a record.  They go
+  // through the warp's free stage `at`, so that rows leave in whole lines (64 stores of 8 bytes a lane
+  // from the fragments took 2.6 us).
+  __device__ __forceinline__ void end(const KvDecodeParams& p, int b, int hv, bool whole, int chunk, uint8_t* at, int lane) {
+    constexpr int kPitch = D + 8, kLanes = D / 4;  // floats of a row (rows a quarter of the banks apart); lanes of a row
+    static_assert(kKvRows * kPitch * 4 <= Ring<FMT, D>::kStage, "a stage takes the sums");
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    const int r = lane / 4, t = lane % 4, G = p.pool.H / p.pool.Hkv;
-    const int head = hv % p.groups * kKvRows + r;  // of the KV head's
-    if (head >= G) return;
-    const long long row = (long long)b * p.pool.H + hv / p.groups * G + head;
-    const long long rec = ((long long)chunk + (long long)b * p.pool.Hkv * p.groups + hv) * p.rec_rows + r;
+    const int g = lane / 4, t = lane % 4, G = p.pool.H / p.pool.Hkv;
+    const int head0 = hv % p.groups * kKvRows, rows = min(G - head0, kKvRows);
+    const long long row0 = (long long)b * p.pool.H + hv / p.groups * G + head0;
+    const long long rec0 = ((long long)chunk + (long long)b * p.pool.Hkv * p.groups + hv) * p.rec_rows;
     const float inv = m == __int_as_float(0xff800000) ? 0.f : 1.f / l;
-    if (t == 0) {
-      if (!whole) p.rec_ml[rec] = make_float2(m, l);
-      else if (p.lse) p.lse[row] = kLn2 * (m + log2f(l));
+    if (t == 0 && g < rows) {
+      if (!whole) p.rec_ml[rec0 + g] = make_float2(m, l);
+      else if (p.lse) p.lse[row0 + g] = kLn2 * (m + log2f(l));
     }
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D);
-    float2* part = reinterpret_cast<float2*>(p.rec + rec * D);
-    auto put = [&](int pair, float x, float y) {
-      if (whole) out[pair] = kv_pack<FMT>(x * inv, y * inv);
-      else part[pair] = make_float2(x, y);
-    };
+    float* mine = reinterpret_cast<float*>(at) + g * kPitch;
     if constexpr (!kInt8) {
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) put(4 * n + t, o[n][0] + o[n][2], o[n][1] + o[n][3]);
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<float2*>(mine + 8 * n + 2 * t) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
     } else {
 #pragma unroll
       for (int jj = 0; jj < D / 64; ++jj)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < 8; i += 2)
-            put(4 * (2 * t + e + 8 * jj) + i / 2, o[8 * jj + i][e] + o[8 * jj + i][e + 2],
-                o[8 * jj + i + 1][e] + o[8 * jj + i + 1][e + 2]);
+          for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4*>(mine + 8 * (2 * t + e + 8 * jj) + i) =
+                make_float4(o[8 * jj + i][e] + o[8 * jj + i][e + 2], o[8 * jj + i + 1][e] + o[8 * jj + i + 1][e + 2],
+                            o[8 * jj + i + 2][e] + o[8 * jj + i + 2][e + 2], o[8 * jj + i + 3][e] + o[8 * jj + i + 3][e + 2]);
+    }
+    __syncwarp();
+    for (int r0 = 0; r0 < rows; r0 += 32 / kLanes) {
+      const int r = r0 + lane / kLanes, c = lane % kLanes;
+      const float f = __shfl_sync(0xffffffffu, inv, 4 * min(r, kKvRows - 1));
+      if (r < rows) {
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(at) + r * kPitch + 4 * c);
+        if (whole)
+          reinterpret_cast<uint2*>(p.out + (row0 + r) * D)[c] = make_uint2(kv_pack<FMT>(v.x * f, v.y * f), kv_pack<FMT>(v.z * f, v.w * f));
+        else
+          reinterpret_cast<float4*>(p.rec + (rec0 + r) * D)[c] = v;
+      }
     }
   }
 };
@@ -640,11 +661,14 @@ __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_k
   int wr = 0, rd = 0;
   bool first = true, whole = false;  // the next tile is its piece's first; the piece is a whole sequence
   bool on = true;                    // there are tiles left
+  Page page;
   auto issue = [&]() {
     int4 what = make_int4(0, 0, 0, 0);
     if (on) {
-      const Tile t = tile_of<R::kTok>(p, c, c.tile % R::kParts);
-      if (t.lo < t.hi) load_tile<FMT, D>(p, t, ring + wr * R::kStage, c.tile % R::kParts, lane);
+      const int part = c.tile % R::kParts;
+      if (first || part == 0) page = page_of(p, c, c.tile / R::kParts);
+      const Tile t = tile_of<R::kTok>(page, part);
+      if (t.lo < t.hi) load_tile<FMT, D>(p, t, ring + wr * R::kStage, part, lane);
       what = make_int4(c.b, c.hv, c.chunk, t.lo | t.hi << 8 | kThere);
       if (first) what.w |= kFirst, whole = c.left == c.size;
       if (whole) what.w |= kWhole;
@@ -688,7 +712,8 @@ __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_k
     if (what.w & kFirst) sums.begin(p, what.x, what.y, lane);
     const int lo = what.w & 255, hi = what.w >> 8 & 255;
     if (lo < hi) sums.add(ring + rd * R::kStage, lo, hi, lane);
-    if (what.w & kLast) sums.end(p, what.x, what.y, what.w & kWhole, what.z, lane);
+    if (what.w & kLast)
+      sums.end(p, what.x, what.y, what.w & kWhole, what.z, smem + warp * R::kBytes + rd * R::kStage, lane);
     __syncwarp();  // the stage is free for the next issue
     rd = rd + 1 == R::kStages ? 0 : rd + 1;
   }
