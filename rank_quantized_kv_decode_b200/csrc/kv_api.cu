@@ -293,7 +293,9 @@ starkv_status starkv_kv_select(const starkv_kv_layout* lay, const void* q, const
   p.keep_first = keep_first;
   p.keep_last = keep_last;
   p.sel = sel;
-  // CTAs per (sequence, KV head): four of them fit on an SM; none without a round of pages (64)
+  // CTAs per (sequence, KV head): four of them fit on an SM; none without a round of pages (64).  One, two
+  // and sixteen took 30.7, 26.4 and 38.4 us at 32 x 512 pages and 8 KV heads (256 pairs; two by this rule),
+  // one, four and sixteen 45.5, 18.7 and 12.5 at 1 x 2047 (8 pairs; sixteen).
   const int64_t units = static_cast<int64_t>(batch) * p.pool.Hkv;
   p.cluster = 1;
   while (p.cluster < kSelMaxCluster && units * p.cluster * 2 <= 4 * sms && p.cluster * 64 < max_pages) p.cluster *= 2;

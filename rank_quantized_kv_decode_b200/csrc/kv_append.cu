@@ -4,6 +4,11 @@
 // its cosine and sine come from the fp32 table (a 128-token tile start times an offset inside
 // the tile: one complex product, error about 2e-7).  int8: per token and group of 32 channels the
 // scale fp16(absmax / 127) and the codes rint(x / scale), from the fp32 values.
+//
+// Bound: HBM for prompts (every row read once and written once; 8192 tokens of 32 + 2 x 8 heads of 128 are
+// 202 MB, 31 us at the measured copy rate, and take 45), latency for a decode step (4 us for 32 tokens).
+// A warp's loads of six rounds (24 rows) are in flight together while it looks up the token, its page
+// and its angles; two rounds a warp took 54 us, four 48, twelve 51.
 #include "kv.cuh"
 #include "store_dev.cuh"
 
@@ -12,7 +17,7 @@ namespace {
 
 constexpr int kAppendWarps = 8;
 constexpr int kRounds16 = 6, kRoundsInt8 = 3;  // rounds of a task of many tokens
-constexpr int kFusedBoundsMax = 256;  // tokens up to which one launch does both (see launch below)
+constexpr int kFusedBoundsMax = 32;  // tokens up to which one launch does both (see the launch)
 
 // A row is one head of q, k or v of a token; D/16 lanes share it, lane j with channels [8j, 8j+8) of
 // each half: both members of a pair, 16-byte accesses, and a scale group is four neighbouring lanes.
@@ -26,7 +31,8 @@ struct Raw {
 };
 template <int D>
 __device__ __forceinline__ Raw load_raw(const uint16_t* row, int j) {
-  return {*reinterpret_cast<const uint4*>(row + 8 * j), *reinterpret_cast<const uint4*>(row + D / 2 + 8 * j)};
+  // read once: leaves L2 to what is written
+  return {__ldcs(reinterpret_cast<const uint4*>(row + 8 * j)), __ldcs(reinterpret_cast<const uint4*>(row + D / 2 + 8 * j))};
 }
 
 // Cosines and sines of a position for the lane's eight pairs.
@@ -177,12 +183,14 @@ __device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, in
         x.from_codes(fa, fz, *reinterpret_cast<const uint2*>(tile + r * D + 8 * j),
                      *reinterpret_cast<const uint2*>(tile + r * D + D / 2 + 8 * j));
       }
-      __half sa, sz;
-      x.scales(sa, sz);  // the whole warp shuffles
-      if (m >= 0) {
-        uint32_t ca[2], cz[2];
-        x.codes(__half2float(sa), __half2float(sz), ca, cz);
-        x.from_codes(__half2float(sa), __half2float(sz), make_uint2(ca[0], ca[1]), make_uint2(cz[0], cz[1]));
+      if (__any_sync(0xffffffffu, m >= 0)) {
+        __half sa, sz;
+        x.scales(sa, sz);  // the whole warp shuffles
+        if (m >= 0) {
+          uint32_t ca[2], cz[2];
+          x.codes(__half2float(sa), __half2float(sz), ca, cz);
+          x.from_codes(__half2float(sa), __half2float(sz), make_uint2(ca[0], ca[1]), make_uint2(cz[0], cz[1]));
+        }
       }
       raw = x.rounded();
     }
@@ -308,10 +316,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROUNDS > 4 || BOUNDS ? 2 : 
 }
 
 // Bounds of the pages that an append of many tokens completed, after it: all keys are in the pages.  A
-// CTA looks at 64 tokens for those in slot 63 (one in 64 of a prompt's) and reads one KV head of their
-// pages, eight rows a warp.
+// CTA looks at `span` tokens for those in slot 63 and reads one KV head of their pages, eight rows a warp.
+// (A warp per token and head read a page alone: 55 us for an 8192-token append instead of 45.)
 template <int FMT, int D>
-__global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p) {
+__global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p, int span) {
   constexpr int CH = FMT == STARKV_KV_INT8 ? 16 : 8;  // channels of a 16-byte load
   constexpr int CPR = D / CH, RPW = 32 / CPR;         // loads per row, rows per warp and load
   __shared__ int hit[kPage];
@@ -323,8 +331,8 @@ __global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p) 
   pdl_launch_dependents();
   if (threadIdx.x == 0) hits = 0;
   __syncthreads();
-  if (threadIdx.x < kPage) {
-    const int n = blockIdx.x * kPage + threadIdx.x;
+  if ((int)threadIdx.x < span) {
+    const int n = blockIdx.x * span + threadIdx.x;
     if (n < p.n_tok && in_table(P, p.tok_seq[n], p.tok_pos[n]) && p.tok_pos[n] % kPage == kPage - 1)
       hit[atomicAdd(&hits, 1)] = n;
   }
@@ -438,12 +446,17 @@ cudaError_t append_rounds(const KvAppendParams& p, cudaStream_t s) {
 
 template <int FMT, int D>
 cudaError_t append_launch(const KvAppendParams& p, cudaStream_t s) {
-  // Few tokens (decode steps, short prompts): the bounds in the same launch, where a completed page's
-  // warp looks through the call's tokens.  Many: a launch behind it.
+  // Few tokens: the bounds in the same launch, where a completed page's warps look through the call's
+  // tokens.  More: a launch behind it.  One launch and two took 2.8 and 4.7 us for 32 bf16 tokens of one
+  // sequence, 4.1 and 6 for 32 sequences that all complete a page, but 7.3 and 5.8 for 64 of one sequence,
+  // whose keys each of those warps makes again.
   if (p.n_tok <= kFusedBoundsMax) return append_rounds<FMT, D, true, 2>(p, s);
   const cudaError_t e = append_rounds<FMT, D, false, FMT == STARKV_KV_INT8 ? kRoundsInt8 : kRounds16>(p, s);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kv_bounds_kernel<FMT, D>, dim3((p.n_tok + kPage - 1) / kPage, p.pool.Hkv), dim3(256), 0, s, p);
+  // About 64 CTAs a KV head: a CTA takes its completed pages one after another, of a prompt one in 64 tokens,
+  // of a batch of sequences all at once.
+  const int span = p.n_tok < 128 ? 2 : p.n_tok > 64 * kPage ? kPage : p.n_tok / 64;
+  return launch_pdl(kv_bounds_kernel<FMT, D>, dim3((p.n_tok + span - 1) / span, p.pool.Hkv), dim3(256), 0, s, p, span);
 }
 
 }  // namespace

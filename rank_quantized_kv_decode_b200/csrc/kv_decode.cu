@@ -12,17 +12,23 @@
 // (bf16) or 22 (fp16) at no further instruction.  tcgen05 would give the same products of 8 rows a
 // 128-row tile.
 //
-// Split: a warp works alone.  Its unit is a tile of 16 tokens (int8: 32) of one KV head; the tiles of
-// all sequences and KV heads form one list, cut into chunks of equal length wherever the sequences
-// begin, and a chunk's part of one sequence and head is a piece.  Lengths are known on the device only, so
-// every warp derives the list from them.  Chunks are the same whoever takes them, so results do not hang
-// on timing; who takes them does: warp w starts with chunk w and draws the next from a counter.  (Equal
-// static shares left SMs idle at the end: at 32 x 32768 tokens they ended between 497 and 646 us.)  A
-// piece that is a whole sequence is written out at once, else as a partial record, and the join adds the
-// records of a sequence in order.  Each warp has its own ring of tiles in shared memory, filled by
-// cp.async, and no barrier with another: four warps that shared a page met once per piece, 1.6 us of a CTA's
-// loads each.  (TMA copies of the same tiles, issued by one lane: no faster at 32 x 32768 tokens, 628 us
-// against 621, and slower for short ones, 22.1 us against 19.4 at a ragged fp16 batch.)
+// Split: a warp works alone.  Its unit is a tile of 16 tokens (int8: 32) of one KV head; the tiles of all
+// sequences and KV heads form one list, cut into chunks wherever the sequences begin, and a chunk's part
+// of one sequence and head is a piece.  Lengths are known on the device only, so every warp derives the
+// list from them.  Chunks are the same whoever takes them, so results do not hang on timing; who takes
+// them does: warp w starts with the large chunk w and draws small ones from a counter.  (SMs get
+// different shares of the memory's rate: with equal static shares of 32 x 32768 tokens they ended
+// between 497 and 646 us; drawing the last quarter took the call from 652 to 612.)  A piece that is a
+// whole sequence is written out at once, else as a partial record, and the join adds the records of a
+// sequence in order.  Each warp has its own ring of tiles in shared memory, filled by cp.async, and no
+// barrier with another: four warps that shared a page met once per piece, 1.6 us of a CTA's loads each.
+// (TMA copies of the same tiles, issued by one lane: no faster at 32 x 32768 tokens and slower for short
+// ones, 22.1 us against 19.4 at a ragged fp16 batch.)
+//
+// Measured: 7.0 TB/s at 32 x 32768 bf16 tokens with 8 KV heads (612 us), 6.2 at 8 x 4096 with 32 (86 us:
+// 4.6 us until the first tile and 3 of the join count there), 4.3 at 131072 int8 tokens (66 us).  int8 is
+// bound by the warps' own instructions: two warps a scheduler (64 fp32 sums a lane for d 128) at half
+// the issue rate, most of it decoding codes; twelve warps an SM spilled and took 92 us.
 #include "kv.cuh"
 
 namespace starkv {
@@ -30,9 +36,12 @@ namespace {
 
 constexpr float kLazy = 8.f;  // the reference follows the running maximum when that is 2^8 above it:
                               // weights stay below 2^8, and O is rescaled a few times per sequence
-constexpr unsigned kStatic = 40;    // tiles a warp below which there are large chunks only
-constexpr unsigned kDrawnPart = 4;  // one tile in so many belongs to a small chunk
-constexpr int kSmall = 8;           // tiles of a small chunk at least; at most kKvRounds of them a warp, about
+// Tiles a warp from which on some are drawn: at 55 (8 x 4096 tokens, 32 KV heads) drawing took 88.6 us and
+// equal shares 92.8, at 28 (131072 int8 tokens, 8 KV heads) drawing took 91 and equal shares 74.
+constexpr unsigned kStatic = 40;
+constexpr unsigned kDrawnPart = 4;  // one tile in so many is drawn: one in 2, 3, 4 took 634, 626, 621 us at 32 x 32768
+constexpr int kSmall = 8;           // tiles of a drawn chunk at least (4: 92.3 us at 8 x 4096, 8: 90.2); at most
+                                    // kKvRounds chunks a warp, about
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Weights of fp16 products are scaled by 2^7 (the factor is part of the reference): with kLazy they

@@ -251,10 +251,10 @@ def test_token_by_token_and_read_back_equal_one_call(fmt):
 
 @pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
 def test_one_launch_and_two_leave_the_same_pages(fmt):
-    # 256 tokens are stored and bounded in one launch, 257 in two; and in calls of 100
+    # 32 tokens are stored and bounded in one launch, 33 in two; and in calls of 100
     cs = [Case(fmt, 4, 2, 128, [400], seed=5) for _ in range(3)]
     k, v = cs[0].draw(400, 2), cs[0].draw(400, 2)
-    for c, cut in zip(cs, ([0, 400], [0, 256, 400], [0, 100, 200, 300, 400])):
+    for c, cut in zip(cs, ([0, 400], list(range(0, 385, 32)) + [400], [0, 100, 200, 300, 400])):
         for a, b in zip(cut, cut[1:]):
             c.append(k[a:b], v[a:b], np.zeros(b - a), np.arange(a, b))
     assert np.array_equal(cs[0].pages(), cs[1].pages()) and np.array_equal(cs[0].pages(), cs[2].pages())
@@ -288,6 +288,27 @@ def test_int8_codes_at_the_edges():
     page, slot = c.table_np[0][np.arange(300) // 64], np.arange(300) % 64
     assert np.array_equal(scales[page, :, slot], ws)
     assert np.array_equal(codes[page, :, slot], wc)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
+@pytest.mark.parametrize("batch", [5, 32, 33, 300])
+def test_a_batch_that_completes_its_pages_together(fmt, batch):
+    # one launch up to 32 tokens, two beyond; every token stands in slot 63
+    c = Case(fmt, 4, 2, 64, [64] * batch, seed=batch)
+    n = 64 * batch
+    k, v = c.draw(n, 2), c.draw(n, 2)
+    seq, pos = np.repeat(np.arange(batch), 64), np.tile(np.arange(64), batch)
+    early, last = np.flatnonzero(pos < 63), np.flatnonzero(pos == 63)
+    c.append(k[early], v[early], seq[early], pos[early])
+    assert np.all(c.pages()[:, :c.olay["off_heads"]] == 0xFF)  # no page is complete, no bounds are written
+    c.append(k[last], v[last], seq[last], pos[last])
+    keys, _ = K.read_tokens(c.pages(), c.olay)
+    b = K.read_bounds(c.pages(), c.olay)
+    p = c.table_np[:, 0]
+    lo, hi = keys[p].min(2), keys[p].max(2)
+    if fmt == "int8":
+        lo, hi = (f64(torch.from_numpy(x).bfloat16()) for x in (lo, hi))
+    assert np.array_equal(b[p][:, :, 0], lo) and np.array_equal(b[p][:, :, 1], hi)
 
 
 def test_rewriting_slot_63_renews_the_bounds():
