@@ -4,7 +4,7 @@
 
 namespace starkv {
 
-constexpr int kKvRows = 8;         // query heads of one KV head that a CTA takes together
+constexpr int kKvRows = 8;         // query heads of one KV head that a warp takes together
 // CTAs of the split kernel on an SM (by its registers; a third one took a ragged batch with d 64 from 16.5 to
 // 14.1 us, and 32 x 32768 tokens with d 128 from 618 to 637), and the most of a launch, on 148 SMs.
 constexpr int kv_split_ctas(int d) { return d == 64 ? 3 : 2; }

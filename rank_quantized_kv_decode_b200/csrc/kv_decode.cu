@@ -233,7 +233,7 @@ __device__ __forceinline__ void load_pages(const KvDecodeParams& p, Piece& c, in
     c.at = c.s.first + i;
     if (p.sel) c.at = p.sel[((long long)c.b * p.pool.Hkv + c.hv / p.groups) * p.n_sel + i];
     if (c.at >= 0 && c.at < (c.s.len + kPage - 1) / kPage) {
-      c.page = p.pool.block_table[(long long)c.b * p.pool.max_pages + c.at];  // looked at by tile_of
+      c.page = p.pool.block_table[(long long)c.b * p.pool.max_pages + c.at];  // looked at by page_of
     } else if (c.at != -1) {
       atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
       c.at = -1;
@@ -692,7 +692,9 @@ __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_k
           int id = list.n;
           if (list.n > workers) {
             const unsigned long long d = __shfl_sync(0xffffffffu, drawn, 0);
-            id = (d >> 32) == (kTag >> 32) ? workers + static_cast<int>(d & 0xffffffffull) : worker + drawn_for * workers;
+            const unsigned before = static_cast<unsigned>(d);  // drawn before it; held below n whatever stood there
+            if ((d >> 32) != (kTag >> 32)) id = worker + drawn_for * workers;
+            else if (before < static_cast<unsigned>(list.n)) id = workers + static_cast<int>(before);
           }
           on = id < list.n;
           if (on) {
