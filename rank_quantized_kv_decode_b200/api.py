@@ -339,14 +339,13 @@ def _kv_arg(t, name: str, dtype, least: int, dev: int) -> int | None:
     """Pointer of a contiguous argument of ``dtype`` with at least ``least`` elements on ``dev``."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() < least:
-        _need(t, name, dtype, least)
+    if t.dtype is dtype and t.numel() >= least and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, dtype, least)
     if t.get_device() != dev:
         raise ValueError("expected a CUDA tensor" if t.get_device() < 0 else
                          f"{name}: tensor on {t.device}, but the cache is on cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError("expected a contiguous tensor")
 
 
 def _kv_rows(t, name: str, dtype, n_tok: int, heads: int, d: int, dev: int) -> tuple[int | None, int]:

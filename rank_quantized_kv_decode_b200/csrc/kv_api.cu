@@ -79,12 +79,10 @@ starkv_status check_kv_layout(const starkv_kv_layout* lay) {
 
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-// The arguments that every call on the pages shares.
+// The arguments that every call on the pages shares (the layout is checked).
 starkv_status fill_pool(const starkv_kv_layout* lay, const void* cache, int64_t num_pages,
                         const int32_t* block_table, int32_t max_pages, int32_t batch,
                         int32_t* dev_status, KvPool& p) {
-  const starkv_status st = check_kv_layout(lay);
-  if (st != STARKV_OK) return st;
   if (max_pages < 1 || max_pages > (1 << 24)) return fail(STARKV_ERR_INVALID_ARG, "max_pages outside [1, 2^24]");
   if (num_pages < 1 || num_pages > INT32_MAX) return fail(STARKV_ERR_INVALID_ARG, "num_pages outside [1, 2^31)");
   if (!cache || !block_table || !dev_status) return fail(STARKV_ERR_INVALID_ARG, "NULL pointer argument");
