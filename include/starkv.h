@@ -459,7 +459,7 @@ typedef struct {
 typedef struct {
   size_t cache_bytes;            /* num_pages * page_bytes                                   */
   size_t rope_table_bytes;       /* table for positions < max_pages * 64                     */
-  size_t decode_workspace_bytes; /* partial records of a decode call of this batch, max_pages */
+  size_t decode_workspace_bytes; /* partial records of a decode call of this batch           */
 } starkv_kv_sizes;
 
 /* Host only, pure. */
@@ -541,7 +541,7 @@ typedef struct {
  *             with a window (INVALID_ARG)
  *   out       device [batch][H][d] in the type of q
  *   lse       device fp32 [batch][H]: ln sum_t exp(scale q_h . k_t), or NULL
- *   workspace device, >= decode_workspace_bytes for this call's batch and max_pages; two calls
+ *   workspace device, >= decode_workspace_bytes for this call's batch; two calls
  *             that may overlap on the GPU need two.  It needs no initial values
  * An empty sequence gives zeros and -inf.  Tokens of a bad block-table entry are flagged and
  * skipped; a seq_len above max_pages * 64 is flagged and cut.  Rows of the last page behind the

@@ -36,6 +36,7 @@ struct KvAppendParams {
   const int *tok_seq, *tok_pos;
   const float2* rope;  // fine [128][d/2] then base [tiles][d/2]
   uint16_t* q_out;     // [n_tok][H][d]
+  int sms;             // of the device
 };
 
 struct KvGatherParams {

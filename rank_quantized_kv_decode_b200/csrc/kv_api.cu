@@ -195,7 +195,9 @@ starkv_status starkv_kv_append(const starkv_kv_layout* lay, const void* q, int64
   if (st != STARKV_OK) return st;
   if (n_tok < 0 || batch < 1) return fail(STARKV_ERR_INVALID_ARG, "n_tok < 0 or batch < 1");
   if (n_tok == 0) return STARKV_OK;
-  if (n_tok > (1 << 24)) return fail(STARKV_ERR_INVALID_ARG, "n_tok too large for one call; split the tokens");
+  // the kernels number their tasks (at most the rows, and two per KV head) in 32 bits
+  if (static_cast<int64_t>(n_tok) * (lay->cfg.n_q_heads + 4 * lay->cfg.n_kv_heads) > INT32_MAX)
+    return fail(STARKV_ERR_INVALID_ARG, "n_tok too large for one call; split the tokens");
   KvAppendParams p;
   std::memset(&p, 0, sizeof(p));
   st = fill_pool(lay, cache, num_pages, block_table, max_pages, batch, dev_status, p.pool);
@@ -226,6 +228,7 @@ starkv_status starkv_kv_append(const starkv_kv_layout* lay, const void* q, int64
   p.tok_pos = tok_pos;
   p.rope = reinterpret_cast<const float2*>(rope_table);
   p.q_out = reinterpret_cast<uint16_t*>(q_out);
+  p.sms = sms;
   const cudaError_t e = launch_kv_append(p, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv append launch");
   return STARKV_OK;

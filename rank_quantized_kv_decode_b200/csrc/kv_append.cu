@@ -6,9 +6,13 @@
 // scale fp16(absmax / 127) and the codes rint(x / scale), from the fp32 values.
 //
 // Bound: HBM for prompts (every row read once and written once; 8192 tokens of 32 + 2 x 8 heads of 128 are
-// 202 MB, 31 us at the measured copy rate, and take 45), latency for a decode step (4 us for 32 tokens).
-// A warp's loads of six rounds (24 rows) are in flight together while it looks up the token, its page
-// and its angles; two rounds a warp took 54 us, four 48, twelve 51.
+// 202 MB, 31 us at the measured copy rate, and take 41), latency for a decode step (4 us for 32 tokens).
+// A warp's loads of eight rounds (32 rows) are in flight together while it looks up the token, its page
+// and its angles; four rounds a warp took 44.5 us, six 42.6, ten 44.1, twelve 50.2.  Of int8, whose rounds
+// hold their rows' ranges and codes as well, 1005 tokens took 27 us with their gather at three rounds, 29 at
+// two and four, 30 at six.
+#include <algorithm>
+
 #include "kv.cuh"
 #include "store_dev.cuh"
 
@@ -16,7 +20,7 @@ namespace starkv {
 namespace {
 
 constexpr int kAppendWarps = 8;
-constexpr int kRounds16 = 6, kRoundsInt8 = 3;  // rounds of a task of many tokens
+constexpr int kRounds16 = 8, kRoundsInt8 = 3;  // rounds of a task of many tokens
 constexpr int kFusedBoundsMax = 32;  // tokens up to which one launch does both (see the launch)
 
 // A row is one head of q, k or v of a token; D/16 lanes share it, lane j with channels [8j, 8j+8) of
@@ -215,28 +219,32 @@ __device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, in
   }
 }
 
+// CTAs on an SM, by the registers that the rounds in flight take.
+constexpr int append_ctas(bool bounds, int rounds) { return rounds > 4 || bounds ? 2 : rounds > 2 ? 3 : 4; }
+
 // One warp per task of ROUNDS rounds of a token's rows, their loads in flight together (`slices` tasks a
-// token); behind them, with BOUNDS, D / 64 warps per (token, KV head) that do something where the token
-// completes its page.
+// token), the tasks in turn where there are more than warps (42.6 us instead of 44.5 for 8192 tokens); behind
+// them, with BOUNDS, D / 64 warps per (token, KV head) that do something where the token completes its page.
 template <int FMT, int D, bool BOUNDS, int ROUNDS>
-__global__ void __launch_bounds__(32 * kAppendWarps, ROUNDS > 4 || BOUNDS ? 2 : ROUNDS > 2 ? 3 : 4)
+__global__ void __launch_bounds__(32 * kAppendWarps, append_ctas(BOUNDS, ROUNDS))
     kv_append_kernel(const KvAppendParams p, int slices) {
   using R = RowMap<D>;
   constexpr int kTask = R::kRows * ROUNDS;
   __shared__ short s_map[BOUNDS ? kAppendWarps : 1][kPage];
   const KvPool& P = p.pool;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  long long task = (long long)blockIdx.x * kAppendWarps + warp;
-  const long long stores = (long long)p.n_tok * slices;
+  // fewer than 2^31 tasks: checked by the caller
+  unsigned task = blockIdx.x * kAppendWarps + warp;
+  const unsigned stores = static_cast<unsigned>(p.n_tok) * slices;
   pdl_wait();
   pdl_launch_dependents();
   if (task >= stores) {
     if (!BOUNDS) return;
     task -= stores;
-    const int side = static_cast<int>(task % (D / 64));
+    const int side = task % (D / 64);
     task /= D / 64;
-    if (task >= (long long)p.n_tok * P.Hkv) return;
-    const int n = static_cast<int>(task / P.Hkv), g = static_cast<int>(task % P.Hkv);
+    const int n = task / P.Hkv, g = task - n * P.Hkv;
+    if (n >= p.n_tok) return;
     const int b = p.tok_seq[n], pos = p.tok_pos[n];
     if (!in_table(P, b, pos) || pos % kPage != kPage - 1) return;
     uint8_t* page = kv_page(P, b, pos / kPage);
@@ -251,73 +259,77 @@ __global__ void __launch_bounds__(32 * kAppendWarps, ROUNDS > 4 || BOUNDS ? 2 : 
     bounds_in_call<FMT, D>(p, page, g, side, map, lane);
     return;
   }
-  const int n = static_cast<int>(task / slices), slice = static_cast<int>(task % slices);
   const int j = lane % R::kLanes;
-  const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv, first = slice * kTask + lane / R::kLanes;
-  Raw raw[ROUNDS];
+  for (;;) {
+    const int n = task / slices, slice = task - n * slices;
+    const int nq = p.q ? P.H : 0, rows = nq + 2 * P.Hkv, first = slice * kTask + lane / R::kLanes;
+    Raw raw[ROUNDS];
 #pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    const int r = first + i * R::kRows;
-    raw[i].lo = raw[i].hi = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const uint16_t* src = r < nq             ? p.q + n * p.q_stride + r * D
-                            : r < nq + P.Hkv ? p.k + n * p.k_stride + (r - nq) * D
-                                             : p.v + n * p.v_stride + (r - nq - P.Hkv) * D;
-      raw[i] = load_raw<D>(src, j);
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int r = first + i * R::kRows;
+      raw[i].lo = raw[i].hi = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const uint16_t* src = r < nq             ? p.q + n * p.q_stride + r * D
+                              : r < nq + P.Hkv ? p.k + n * p.k_stride + (r - nq) * D
+                                               : p.v + n * p.v_stride + (r - nq - P.Hkv) * D;
+        raw[i] = load_raw<D>(src, j);
+      }
     }
-  }
-  const int b = p.tok_seq[n], pos = p.tok_pos[n];
-  const bool pos_ok = pos >= 0 && pos < P.max_pages * kPage;
-  uint8_t* page = in_table(P, b, pos) ? kv_page(P, b, pos / kPage) : nullptr;
-  if (!page && lane == 0 && slice == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
-  const int slot = pos_ok ? pos % kPage : 0;
-  float2 c[8];
+    const int b = p.tok_seq[n], pos = p.tok_pos[n];
+    const bool pos_ok = pos >= 0 && pos < P.max_pages * kPage;
+    uint8_t* page = in_table(P, b, pos) ? kv_page(P, b, pos / kPage) : nullptr;
+    if (!page && lane == 0 && slice == 0) atomicOr(P.status, STARKV_DEV_BOUNDS);
+    const int slot = pos_ok ? pos % kPage : 0;
+    float2 c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = make_float2(0.f, 0.f);
-  if (pos_ok) angles<D>(p.rope, pos, j, c);
+    for (int i = 0; i < 8; ++i) c[i] = make_float2(0.f, 0.f);
+    if (pos_ok) angles<D>(p.rope, pos, j, c);
 #pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    const int r = first + i * R::kRows;
-    if (slice * kTask + i * R::kRows >= rows) break;  // the same for the whole warp
-    const bool in = r < rows;
-    const int kind = r < nq ? 0 : (r < nq + P.Hkv ? 1 : 2);
-    const int h = kind == 0 ? r : (kind == 1 ? r - nq : r - nq - P.Hkv);
-    Row<FMT> x;
-    x.set(raw[i]);
-    if (kind != 2) x.rotate(c);
-    uint8_t* tile = page + P.off_heads + (long long)h * P.head_bytes + (kind == 2 ? P.off_v : 0);
-    uint16_t* dst = nullptr;
-    if (kind == 0)
-      dst = p.q_out + ((long long)n * P.H + h) * D;
-    else if (FMT != STARKV_KV_INT8 && page)
-      dst = reinterpret_cast<uint16_t*>(tile) + slot * D;
-    if (in && dst) {
-      const Raw o = x.rounded();
-      *reinterpret_cast<uint4*>(dst + 8 * j) = o.lo;
-      *reinterpret_cast<uint4*>(dst + D / 2 + 8 * j) = o.hi;
-    }
-    if (FMT == STARKV_KV_INT8 && slice * kTask + (i + 1) * R::kRows > nq) {  // not a round of queries alone
-      __half sa, sz;
-      x.scales(sa, sz);  // the whole warp shuffles
-      if (in && kind != 0 && page) {
-        uint32_t ca[2], cz[2];
-        x.codes(__half2float(sa), __half2float(sz), ca, cz);
-        *reinterpret_cast<uint2*>(tile + slot * D + 8 * j) = make_uint2(ca[0], ca[1]);
-        *reinterpret_cast<uint2*>(tile + slot * D + D / 2 + 8 * j) = make_uint2(cz[0], cz[1]);
-        if (j % 4 == 0) {
-          __half* sc = reinterpret_cast<__half*>(page + P.off_heads + (long long)h * P.head_bytes +
-                                                 (kind == 2 ? P.off_vs : P.off_ks)) + slot * (D / 32);
-          sc[j / 4] = sa;
-          sc[D / 64 + j / 4] = sz;
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int r = first + i * R::kRows;
+      if (slice * kTask + i * R::kRows >= rows) break;  // the same for the whole warp
+      const bool in = r < rows;
+      const int kind = r < nq ? 0 : (r < nq + P.Hkv ? 1 : 2);
+      const int h = kind == 0 ? r : (kind == 1 ? r - nq : r - nq - P.Hkv);
+      Row<FMT> x;
+      x.set(raw[i]);
+      if (kind != 2) x.rotate(c);
+      uint8_t* tile = page + P.off_heads + (long long)h * P.head_bytes + (kind == 2 ? P.off_v : 0);
+      uint16_t* dst = nullptr;
+      if (kind == 0)
+        dst = p.q_out + ((long long)n * P.H + h) * D;
+      else if (FMT != STARKV_KV_INT8 && page)
+        dst = reinterpret_cast<uint16_t*>(tile) + slot * D;
+      if (in && dst) {
+        const Raw o = x.rounded();
+        *reinterpret_cast<uint4*>(dst + 8 * j) = o.lo;
+        *reinterpret_cast<uint4*>(dst + D / 2 + 8 * j) = o.hi;
+      }
+      if (FMT == STARKV_KV_INT8 && slice * kTask + (i + 1) * R::kRows > nq) {  // not a round of queries alone
+        __half sa, sz;
+        x.scales(sa, sz);  // the whole warp shuffles
+        if (in && kind != 0 && page) {
+          uint32_t ca[2], cz[2];
+          x.codes(__half2float(sa), __half2float(sz), ca, cz);
+          *reinterpret_cast<uint2*>(tile + slot * D + 8 * j) = make_uint2(ca[0], ca[1]);
+          *reinterpret_cast<uint2*>(tile + slot * D + D / 2 + 8 * j) = make_uint2(cz[0], cz[1]);
+          if (j % 4 == 0) {
+            __half* sc = reinterpret_cast<__half*>(page + P.off_heads + (long long)h * P.head_bytes +
+                                                   (kind == 2 ? P.off_vs : P.off_ks)) + slot * (D / 32);
+            sc[j / 4] = sa;
+            sc[D / 64 + j / 4] = sz;
+          }
         }
       }
     }
+    task += gridDim.x * kAppendWarps;
+    if (task >= stores) return;
   }
 }
 
 // Bounds of the pages that an append of many tokens completed, after it: all keys are in the pages.  A
 // CTA looks at `span` tokens for those in slot 63 and reads one KV head of their pages, eight rows a warp.
-// (A warp per token and head read a page alone: 55 us for an 8192-token append instead of 45.)
+// (A warp per token and head read a page alone: 55 us for an 8192-token append where this took 45, its stores then 4 us slower.)
 template <int FMT, int D>
 __global__ void __launch_bounds__(256) kv_bounds_kernel(const KvAppendParams p, int span) {
   constexpr int CH = FMT == STARKV_KV_INT8 ? 16 : 8;  // channels of a 16-byte load
@@ -439,8 +451,9 @@ cudaError_t append_rounds(const KvAppendParams& p, cudaStream_t s) {
   constexpr int kTask = RowMap<D>::kRows * ROUNDS;
   const int rows = (p.q ? p.pool.H : 0) + 2 * p.pool.Hkv, slices = (rows + kTask - 1) / kTask;
   const long long tasks = (long long)p.n_tok * (slices + (BOUNDS ? p.pool.Hkv * (D / 64) : 0));
-  return launch_pdl(kv_append_kernel<FMT, D, BOUNDS, ROUNDS>,
-                    dim3(static_cast<unsigned>((tasks + kAppendWarps - 1) / kAppendWarps)), dim3(32 * kAppendWarps), 0, s,
+  long long ctas = (tasks + kAppendWarps - 1) / kAppendWarps;
+  if (!BOUNDS) ctas = std::min<long long>(ctas, static_cast<long long>(p.sms) * append_ctas(BOUNDS, ROUNDS));
+  return launch_pdl(kv_append_kernel<FMT, D, BOUNDS, ROUNDS>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kAppendWarps), 0, s,
                     p, slices);
 }
 

@@ -95,7 +95,7 @@ def append(lib, lay, q=P16, qs=1024, k=P16, ks=256, v=P16, vs=256, n=1, seq=P16,
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(n=-1), L.ERR_INVALID_ARG), (dict(n=(1 << 24) + 1), L.ERR_INVALID_ARG), (dict(batch=0), L.ERR_INVALID_ARG), (dict(mp=0), L.ERR_INVALID_ARG),
+    (dict(n=-1), L.ERR_INVALID_ARG), (dict(n=(1 << 31) // 16), L.ERR_INVALID_ARG), (dict(batch=0), L.ERR_INVALID_ARG), (dict(mp=0), L.ERR_INVALID_ARG),
     (dict(mp=(1 << 24) + 1), L.ERR_INVALID_ARG), (dict(pages=0), L.ERR_INVALID_ARG),
     (dict(k=None), L.ERR_INVALID_ARG), (dict(v=None), L.ERR_INVALID_ARG), (dict(seq=None), L.ERR_INVALID_ARG),
     (dict(pos=None), L.ERR_INVALID_ARG), (dict(bt=None), L.ERR_INVALID_ARG), (dict(rope=None), L.ERR_INVALID_ARG),
