@@ -16,9 +16,12 @@
 // Bound: HBM for large batches (the bounds are 4 d bytes per page and KV head, read once), latency
 // for one sequence.  32 sequences x 512 pages x 8 KV heads take 26 us (67 MB, 10 us at the measured copy
 // rate): 14 until all is scored, then 6 for the choice; one sequence of 2047 pages 12.5.  Bounds through a
-// cp.async ring, always two rounds in flight, scored no faster (26 to 30 us).  A cluster of CTAs shares one (sequence, KV head): each scores its share of the
-// pages into the first CTA's shared memory, which then chooses.
+// cp.async ring, always two rounds in flight, scored no faster (26 to 30 us).  A cluster of CTAs shares one
+// (sequence, KV head): each scores its share of the pages into the first CTA's shared memory, which then
+// chooses.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "kv.cuh"
 
@@ -133,6 +136,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelec
   const int rank = blockIdx.x % p.cluster, unit = blockIdx.x / p.cluster;
   const int b = unit / P.Hkv, g = unit % P.Hkv, G = P.H / P.Hkv;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, row = lane / 4, t = lane % 4;
+  auto started = cluster.barrier_arrive();
   pdl_wait();
   pdl_launch_dependents();
   const int raw = p.seq_lens[b];
@@ -158,6 +162,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelec
   // ---- fp32 scores, and the largest sum |q_c| of a head (every warp for itself)
   float q1 = 0.f;
   {
+    cluster.barrier_wait(std::move(started));  // the first CTA's shared memory is there once it has started
     uint32_t* first = cluster.map_shared_rank(keys, 0);
     uint32_t mag = 0;
     for (int i = threadIdx.x; i < kBins; i += kSelThreads) s_bins[i] = 0;
