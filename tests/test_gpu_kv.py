@@ -175,7 +175,7 @@ def near_codes(codes, scales, want, tol):
 @pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
 @pytest.mark.parametrize("H,Hkv,d,news", [
     (8, 2, 128, [1, 64, 65, 130]), (4, 4, 64, [63, 1, 3]), (10, 2, 128, [200]), (64, 1, 64, [5, 7]),
-    (32, 32, 128, [2, 700])])
+    (32, 32, 128, [2, 700]), (6, 1, 64, [2601, 2502])])  # the last: more tasks than warps
 def test_append_stores_rotated_keys_values_and_bounds(fmt, H, Hkv, d, news):
     lens = [n + 61 * i for i, n in enumerate(news)]  # sequence i starts at position 61 i
     c = Case(fmt, H, Hkv, d, lens, seed=3)
