@@ -547,8 +547,10 @@ typedef struct {
  * skipped; a seq_len above max_pages * 64 is flagged and cut.  Rows of the last page behind the
  * sequence, and before the window, are never read into a sum, whatever they hold; an infinite
  * value that does count gives an infinity or a NaN in its channel.
- * Two launches: a split kernel, whose CTAs draw chunks of the batch's pages, and a join of the
- * sequences that were split.  Results do not depend on timing. */
+ * Two launches: a split kernel, whose warps take chunks of a list of all tiles (pieces of a page of one
+ * KV head) and draw the last ones where the list is long, and a join of the sequences that were split;
+ * where max_pages, the window or the selection allow such a list, a third before them, which sets the
+ * counter of the draws.  Results do not depend on timing. */
 STARKV_API starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q,
                                           const void* cache, int64_t num_pages,
                                           const int32_t* block_table, int32_t max_pages,

@@ -65,7 +65,7 @@ struct KvDecodeParams {
   float scale2;     // scale * log2(e)
   uint16_t* out;    // [batch][H][d]
   float* lse;       // [batch][H] or null
-  unsigned long long* counter;  // chunks drawn
+  unsigned* counter;  // chunks drawn
   float* rec;       // [piece][rec_rows][d] partial sums; piece = chunk + flat (sequence, KV head, group)
   float2* rec_ml;   // [piece][rec_rows] reference (log2 units), sum
   int rec_rows;     // query heads of a KV head, at most kKvRows

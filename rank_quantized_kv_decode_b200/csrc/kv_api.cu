@@ -352,7 +352,7 @@ starkv_status starkv_kv_decode(const starkv_kv_layout* lay, const void* q, const
   if (grid > kv_max_ctas(p.pool.d)) grid = kv_max_ctas(p.pool.d);
   if (grid > most) grid = most;
   p.grid = static_cast<int>(grid);
-  p.counter = reinterpret_cast<unsigned long long*>(workspace);
+  p.counter = reinterpret_cast<unsigned*>(workspace);
   p.rec = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + kKvCounterBytes);
   p.rec_rows = kv_record_rows(lay);
   p.rec_ml = reinterpret_cast<float2*>(p.rec + static_cast<size_t>(kv_pieces(lay, batch)) * p.rec_rows * p.pool.d);

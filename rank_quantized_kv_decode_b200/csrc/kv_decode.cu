@@ -29,6 +29,8 @@
 // 4.6 us until the first tile and 3 of the join count there), 4.3 at 131072 int8 tokens (66 us).  int8 is
 // bound by the warps' own instructions: two warps a scheduler (64 fp32 sums a lane for d 128) at half
 // the issue rate, most of it decoding codes; twelve warps an SM spilled and took 92 us.
+#include <algorithm>
+
 #include "kv.cuh"
 
 namespace starkv {
@@ -639,10 +641,12 @@ __device__ __forceinline__ float part_weight(float m, float M) {
 }
 
 
-// The counter of chunks drawn: the upper half says that the lower is one.  The join leaves it at zero;
-// whatever else the workspace holds there before a first call, the tag is missing and the warps take
-// their chunks in a fixed order instead, with the same results.
-constexpr unsigned long long kTag = 0x73744b56ull << 32;
+// Sets the counter of chunks drawn to zero before a split kernel that may draw, whatever the workspace holds.
+__global__ void kv_counter_kernel(unsigned* counter) {
+  pdl_launch_dependents();
+  pdl_wait();
+  *counter = 0;
+}
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_kernel(const KvDecodeParams p) {
@@ -660,11 +664,9 @@ __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_k
   const List list = list_of(p, lane, R::kParts);
   if (worker >= list.n) return;
   Piece c = piece_of(p, list, lane, R::kParts, worker);
-  int drawn_for = 0;             // chunks drawn
-  unsigned long long drawn = 0;  // lane 0: the draw of the chunk after c's, made when c's begins
+  unsigned drawn = 0;  // lane 0: the draw of the chunk after c's, made when c's begins
   auto draw = [&]() {
-    ++drawn_for;
-    if (lane == 0 && list.n > workers) drawn = atomicAdd(p.counter, 1ull);
+    if (lane == 0 && list.n > workers) drawn = atomicAdd(p.counter, 1u);
   };
   draw();
   int wr = 0, rd = 0;
@@ -690,12 +692,8 @@ __global__ void __launch_bounds__(32 * kKvWarps, Ring<FMT, D>::kCtas) kv_split_k
           next_piece(p, c, lane, R::kParts);
         } else {
           int id = list.n;
-          if (list.n > workers) {
-            const unsigned long long d = __shfl_sync(0xffffffffu, drawn, 0);
-            const unsigned before = static_cast<unsigned>(d);  // drawn before it; held below n whatever stood there
-            if ((d >> 32) != (kTag >> 32)) id = worker + drawn_for * workers;
-            else if (before < static_cast<unsigned>(list.n)) id = workers + static_cast<int>(before);
-          }
+          // chunks drawn before it: at most one past the end for each warp
+          if (list.n > workers) id = workers + static_cast<int>(__shfl_sync(0xffffffffu, drawn, 0));
           on = id < list.n;
           if (on) {
             draw();
@@ -755,7 +753,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvDecode
   const int c0 = count ? list.chunk_of(before) : 0, c1 = count ? list.chunk_of(before + count * per_page - 1) : 0;
   pdl_wait();
   pdl_launch_dependents();
-  if (threadIdx.x == 0 && h == 0 && b == 0) *p.counter = kTag;
   if (threadIdx.x == 0 && h == 0 && (raw < 0 || raw > p.pool.max_pages * kPage)) atomicOr(p.pool.status, STARKV_DEV_BOUNDS);
   if (count == 0) {
     if (threadIdx.x < D / 2) reinterpret_cast<uint32_t*>(p.out + row * D)[threadIdx.x] = 0;
@@ -811,11 +808,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const KvDecode
   }
 }
 
+// Whether some lengths make a list of this call that is drawn from (see list_of).
+bool may_draw(const KvDecodeParams& p, int per_page) {
+  long long pages = p.pool.max_pages;
+  if (p.sel) pages = std::min<long long>(pages, p.n_sel);
+  else if (p.window > 0) pages = std::min(pages, (p.window - 1LL + kPage - 1) / kPage + 1);
+  return pages * p.pool.batch * p.pool.Hkv * p.groups * per_page > static_cast<long long>(p.grid) * kKvWarps * kStatic;
+}
+
 template <int FMT, int D>
 cudaError_t decode_launch(const KvDecodeParams& p, cudaStream_t s) {
   using R = Ring<FMT, D>;
   static_assert(R::kCtas * (R::kSmem + 2048) <= 228 * 1024, "the CTAs of an SM share its memory");
   cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<FMT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+  if (e == cudaSuccess && may_draw(p, R::kParts)) e = launch_pdl(kv_counter_kernel, dim3(1), dim3(1), 0, s, p.counter);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_split_kernel<FMT, D>, dim3(p.grid), dim3(32 * kKvWarps), R::kSmem, s, p);
   if (e != cudaSuccess) return e;

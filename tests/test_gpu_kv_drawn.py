@@ -98,6 +98,29 @@ def test_drawing_calls_may_find_anything_in_the_workspace(fmt):
             assert all(torch.equal(x, y) for x, y in zip(want, other)), fill
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "int8"])
+@pytest.mark.parametrize("upper", [0, 1, 0x73744B56])
+def test_a_count_left_in_the_workspace_skips_nothing(fmt, upper):
+    """The first words of a workspace as a call that did not finish might leave them, beside records that
+    are none of this call's."""
+    c = Case(fmt, 8, 2, 128, [3000, 17, 9000, 640], seed=13)
+    assert draws(c, 2)
+    c.fill()
+    q = c.draw(4, 8, 1.5)
+    out, lse = c.decode(q, max_ctas=2)
+    c.check(q, out, lse)
+    ws = c.kv.decode_ws
+    for count in (1, 7, 20, 1 << 20, 0x73744B56, 0xFFFFFFFF):
+        ws.fill_(0xFF)
+        word = torch.tensor(np.array([upper << 32 | count], np.uint64).view(np.int64))
+        ws[:8].view(torch.int64).copy_(word)
+        again, lse2 = c.decode(q, max_ctas=2)
+        assert torch.equal(out, again) and torch.equal(lse, lse2), count
+        again, lse2 = c.decode(q, max_ctas=2)
+        assert torch.equal(out, again) and torch.equal(lse, lse2), count
+    assert c.status() == 0
+
+
 def test_a_captured_call_draws_at_some_lengths_and_not_at_others():
     c = Case("bf16", 8, 2, 128, [5000, 900, 64], seed=3)
     c.fill()
