@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, append_ctas(BOUNDS, ROUNDS)
       else if (FMT != STARKV_KV_INT8 && page)
         dst = reinterpret_cast<uint16_t*>(tile) + slot * D;
       if (in && dst) {
-        const Raw o = x.rounded();
+        Raw o = x.rounded();
+        if (!pos_ok) o.lo = o.hi = make_uint4(0, 0, 0, 0);  // a query's row, whatever it holds (0 x inf is no zero)
         *reinterpret_cast<uint4*>(dst + 8 * j) = o.lo;
         *reinterpret_cast<uint4*>(dst + D / 2 + 8 * j) = o.hi;
       }
