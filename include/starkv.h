@@ -514,8 +514,9 @@ STARKV_API starkv_status starkv_kv_gather(const starkv_kv_layout* lay, const voi
  *            places -1
  * Needs 1 <= keep_last (the last page has no bounds yet), 0 <= keep_first,
  * keep_first + keep_last <= n_sel, and max_pages <= STARKV_KV_MAX_SELECT_PAGES.  Bounds that hold
- * an infinity or NaN give an unspecified choice (of valid pages).  A bad block-table entry is
- * flagged and its page takes the lowest score. */
+ * an infinity or NaN give an unspecified choice (of valid pages).  A bad block-table entry of any page
+ * of the sequence is flagged; a page that would be scored takes the lowest score, one that is always
+ * taken stays in the choice. */
 #define STARKV_KV_MAX_SELECT_PAGES 16384
 STARKV_API starkv_status starkv_kv_select(const starkv_kv_layout* lay, const void* q,
                                           const void* cache, int64_t num_pages,

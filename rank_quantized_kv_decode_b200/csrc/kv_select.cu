@@ -115,6 +115,15 @@ __device__ __forceinline__ double exact_bound(const uint16_t* q, const uint8_t* 
   return a;
 }
 
+// Flags bad ones of n entries of a sequence's block table from the i0-th (whole CTA): those that no scoring
+// looks at.
+__device__ __forceinline__ void flag_unscored(const KvPool& P, int b, int i0, int n) {
+  for (int i = threadIdx.x; i < n; i += kSelThreads) {
+    const int pg = P.block_table[(long long)b * P.max_pages + i0 + i];
+    if (pg < 0 || pg >= P.num_pages) atomicOr(P.status, STARKV_DEV_BOUNDS);
+  }
+}
+
 template <int F, int D>
 __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelectParams p) {
   constexpr int NJ = D / 32;   // 16-byte loads per row and lane
@@ -145,17 +154,21 @@ __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelec
   if (threadIdx.x == 0 && rank == 0 && g == 0 && raw != len) atomicOr(P.status, STARKV_DEV_BOUNDS);
   int* sel = p.sel + (long long)unit * p.n_sel;
   if (pages <= p.n_sel) {  // the same for the whole cluster
-    if (rank == 0)
+    if (rank == 0) {
       for (int i = threadIdx.x; i < p.n_sel; i += kSelThreads) sel[i] = i < pages ? i : -1;
+      if (g == 0) flag_unscored(P, b, 0, pages);
+    }
     return;
   }
   const int c0 = p.keep_first, nc = pages - p.keep_first - p.keep_last;  // candidates [c0, c0 + nc)
   const int want = p.n_sel - p.keep_first - p.keep_last;
   const uint16_t* q = p.q + ((long long)b * P.H + g * G) * D;
   if (want == 0) {
-    if (rank == 0)
+    if (rank == 0) {
       for (int i = threadIdx.x; i < p.n_sel; i += kSelThreads)
         sel[i] = i < p.keep_first ? i : pages - p.n_sel + i;
+      if (g == 0) flag_unscored(P, b, 0, pages);
+    }
     return;
   }
 
@@ -254,6 +267,10 @@ __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelec
     }
   }
   cluster.sync();
+  if (g == 0 && rank == p.cluster - 1) {  // the ends, which are always taken
+    flag_unscored(P, b, 0, p.keep_first);
+    flag_unscored(P, b, pages - p.keep_last, p.keep_last);
+  }
   if (rank != 0) return;
 
   // ---- the bin of the want-th largest key

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import kv_oracle as K
 from rank_quantized_kv_decode_b200 import _lib as L
 from test_gpu_kv import Case, f64, near16, rotated
 
@@ -36,3 +37,27 @@ def test_queries_of_tokens_outside_the_table_become_zeros_whatever_they_hold(fmt
     page = c.table_np[0][pos[~bad] // 64]
     others = np.setdiff1d(np.arange(before.shape[0]), page)
     assert np.array_equal(before[others], c.pages()[others])
+
+
+@pytest.mark.parametrize("width", [9, 200])  # one CTA a choice, and several
+@pytest.mark.parametrize("n,n_sel,first,last,bad", [
+    (64 * 5, 8, 1, 2, 3), (64 * 5, 5, 0, 1, 0), (1, 1, 0, 1, 0), (64 * 5 - 7, 5, 1, 1, 4),  # every page is taken
+    (64 * 9, 3, 1, 2, 0), (64 * 9, 3, 1, 2, 7), (64 * 9, 2, 0, 2, 8), (64 * 9, 3, 1, 2, 4),  # none is scored
+    (64 * 9, 6, 2, 3, 1), (64 * 9, 6, 2, 3, 6), (64 * 9, 6, 2, 3, 8), (64 * 9 - 63, 5, 1, 1, 8),  # kept at an end
+    (64 * 9, 6, 2, 3, 4)])  # scored
+def test_select_flags_a_bad_page_wherever_it_lies(width, n, n_sel, first, last, bad):
+    c = Case("bf16", 4, 2, 64, [64 * 9, n], seed=2, width=width)
+    c.fill()
+    q = c.draw(2, 4)
+    s = K.page_scores(f64(q)[1], K.read_bounds(c.pages(), c.olay)[c.table_np[1, :-(-n // 64)]])
+    c.table[1, -(-n // 64):] = -1  # behind the sequence: no entries of its own
+    c.select(q, n_sel, first, last)
+    assert c.status() == 0
+    for entry in (-1, c.kv.num_pages, 2**31 - 1, -2**31):
+        c.kv.status.zero_()
+        c.table[1, bad] = entry
+        sel = c.select(q, n_sel, first, last).cpu().numpy()
+        assert c.status() == L.DEV_BOUNDS, entry
+        s[:, bad] = -np.inf
+        for g in range(2):
+            assert np.array_equal(sel[1, g], K.choose(s[g], n, n_sel, first, last))
