@@ -35,6 +35,9 @@ constexpr int kSelWarps = kSelThreads / 32;
 // most 17 x 2^-24 of the running magnitude (<= S) where the unit cuts instead of rounding: 16 x 17 x
 // 2^-24 < 2^-15.9 at d = 128.
 constexpr float kScoreError = 1.f / 32768.f;
+// And at the ends of fp32's range: 2 d products and as many sums, each off by at most 2^-126 where they are
+// subnormal (2^9 x 2^-126); where a sum could pass 2^127 the error has no bound, and all pages are scored again.
+constexpr float kScoreFloor = 0x1p-117f, kScoreMost = 0x1p126f;
 constexpr int kRankAll = kSelThreads;  // pages between that are ranked by comparing all pairs
 
 template <bool BF>
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const KvSelec
     const uint32_t k1 = mx - k0 < width ? mx : k0 + width;  // the bin's keys: [k0, k1]
     uint32_t mag = 0;
     for (int r = 0; r < p.cluster; ++r) mag = max(mag, s_mag[r]);
-    const float e2 = 2.f * kScoreError * q1 * kv_unpack<F>(mag).x;
+    const float most = q1 * kv_unpack<F>(mag).x;  // no product or sum of a score is larger
+    const float e2 = most < kScoreMost ? 2.f * (kScoreError * most + kScoreFloor) : __int_as_float(0x7f800000);
     const float v0 = key_value(max(k0, 1u)), v1 = key_value(max(k1, 1u));
     int ins = 0;
     constexpr int kAt = 4;  // keys a thread has in hand

@@ -61,3 +61,25 @@ def test_select_flags_a_bad_page_wherever_it_lies(width, n, n_sel, first, last, 
         s[:, bad] = -np.inf
         for g in range(2):
             assert np.array_equal(sel[1, g], K.choose(s[g], n, n_sel, first, last))
+
+
+@pytest.mark.parametrize("d,H", [(64, 1), (128, 2), (64, 10)])
+@pytest.mark.parametrize("power", [-149, -144, -140, -130, -120, -110, 0, 110, 119, 120, 121, 122, 123, 124])
+def test_select_at_the_ends_of_fp32(power, d, H):
+    """Bounds above zero under queries of both signs: a score is the difference of two sums of about 2^power times the
+    number of channels, which pass fp32's largest number, or fall below its smallest, where the score is exact."""
+    pages = 300
+    c = Case("bf16", H, 1, d, [64 * pages], seed=200 + d + power, fill=0)
+    x = 1.0 + np.abs(c.rng.standard_normal((c.kv.num_pages, 2, d)))
+    x[:, 1] = x[:, 0] * (1 + 0.2 * c.rng.random(x[:, 0].shape))
+    bits = torch.from_numpy(x * 2.0 ** (power // 2)).bfloat16().view(torch.int16).numpy()
+    img = c.pages().copy()
+    img[:, :c.olay["off_heads"]] = bits.reshape(c.kv.num_pages, -1).view(np.uint8)
+    c.kv.cache.copy_(torch.from_numpy(img.reshape(-1)))
+    q = c.draw(1, H, 2.0 ** (power - power // 2))
+    s = K.page_scores(f64(q)[0], K.read_bounds(img, c.olay)[c.table_np[0]])
+    assert np.all(np.isfinite(s)) and len(np.unique(s)) > pages - 3
+    for n_sel in (3, 20, 150, 298):
+        sel = c.select(q, n_sel, 1, 1).cpu().numpy()
+        assert np.array_equal(sel[0, 0], K.choose(s[0], 64 * pages, n_sel, 1, 1)), n_sel
+    assert c.status() == 0
