@@ -385,6 +385,13 @@ def _kv_stream(dev: int, stream) -> int:
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _kv_int(x: int, name: str) -> int:
+    """A number that the library takes in 32 bits; ctypes would cut it to them."""
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name}: {x} does not fit in 32 bits")
+    return x
+
+
 def _kv_sel(lay, sel, batch: int, dev: int) -> tuple[int, int]:
     """(pointer, pages) of a selection [batch][H_kv][pages]."""
     shape = sel.shape
@@ -444,7 +451,7 @@ def kv_select(lay, q, cache, block_table, seq_lens, sel, status, keep_first: int
     L.check(L.load().starkv_kv_select(
         ctypes.byref(lay), _kv_arg(q, "q", _KV_DTYPE[c.fmt], batch * c.n_q_heads * c.head_dim, dev),
         _kv_arg(cache, "cache", cache.dtype, 0, dev), cache.nbytes // lay.page_bytes, table, width, lens, batch,
-        n_sel, keep_first, keep_last, sp, _kv_arg(status, "status", torch.int32, 1, dev),
+        n_sel, _kv_int(keep_first, "keep_first"), _kv_int(keep_last, "keep_last"), sp, _kv_arg(status, "status", torch.int32, 1, dev),
         _kv_stream(dev, stream)), "starkv_kv_select")
 
 
@@ -460,7 +467,10 @@ def kv_decode(lay, q, cache, block_table, seq_lens, out, workspace, status, sel=
     sp, n_sel = _kv_sel(lay, sel, batch, dev) if sel is not None else (None, 0)
     opts = None
     if scale or window or max_ctas:
-        opts = ctypes.byref(L.KvDecodeOpts(scale, window, max_ctas, 0))
+        o = L.KvDecodeOpts(scale, _kv_int(window, "window"), _kv_int(max_ctas, "max_ctas"), 0)
+        if scale and not o.scale:
+            raise ValueError(f"scale: {scale} is 0 in fp32, which stands for 1 / sqrt(head_dim)")
+        opts = ctypes.byref(o)
     L.check(L.load().starkv_kv_decode(
         ctypes.byref(lay), _kv_arg(q, "q", dt, size, dev), _kv_arg(cache, "cache", cache.dtype, 0, dev),
         cache.nbytes // lay.page_bytes, table, width, lens, batch, sp, n_sel, opts,
