@@ -429,7 +429,9 @@ typedef enum {
   STARKV_KV_INT8 = 2  /* q, k, v and results bf16; stored as int8 codes with one fp16 scale
                          per token and group of 32 channels: the quantiser of the int8 part
                          of STARKV_FMT_MIXED, applied to the fp32 rotated key and to the
-                         value.  Values above 65504 in magnitude are not representable       */
+                         value.  The append stores and the gather returns magnitudes up to
+                         127 x 65504; starkv_kv_decode, which rounds code times scale of a
+                         value to fp16, makes an infinity of those above 65504, unflagged    */
 } starkv_kv_fmt;
 
 typedef struct {
@@ -505,8 +507,8 @@ STARKV_API starkv_status starkv_kv_gather(const starkv_kv_layout* lay, const voi
 
 /* Choose pages for sparse attention.  For KV head g and a complete page p,
  *   score(g, p) = max over the query heads h of g of sum_c max(q_h,c lo_p,c, q_h,c hi_p,c),
- * an upper bound of every q_h . k_t in the page, summed in fp64 so that the order of pages does
- * not hang on rounding.  A sequence of P = ceil(seq_len / 64) pages gets all of them when
+ * an upper bound of every q_h . k_t in the page (int8: but for the rounding of the bounds to bf16),
+ * summed in fp64 so that the order of pages does not hang on rounding.  A sequence of P = ceil(seq_len / 64) pages gets all of them when
  * P <= n_sel; else its first keep_first and last keep_last pages and, of the rest, those of
  * the largest score (equal scores: the lower page first), n_sel in all.
  *   q        device [batch][H][d], rotated (q_out of the append)
@@ -547,7 +549,9 @@ typedef struct {
  * An empty sequence gives zeros and -inf.  Tokens of a bad block-table entry are flagged and
  * skipped; a seq_len above max_pages * 64 is flagged and cut.  Rows of the last page behind the
  * sequence, and before the window, are never read into a sum, whatever they hold; an infinite
- * value that does count gives an infinity or a NaN in its channel.
+ * value that does count gives an infinity or a NaN in its channel, and so may finite bf16 values whose
+ * sum, under weights of up to 2^8 and before the division, passes fp32's largest number.
+ * Keys and values are read once for each eight query heads of a KV head.
  * Two launches: a split kernel, whose warps take chunks of a list of all tiles (pieces of a page of one
  * KV head) and draw the last ones where the list is long, and a join of the sequences that were split;
  * where max_pages, the window or the selection allow such a list, a third before them, which sets the

@@ -6,11 +6,11 @@
 // scale fp16(absmax / 127) and the codes rint(x / scale), from the fp32 values.
 //
 // Bound: HBM for prompts (every row read once and written once; 8192 tokens of 32 + 2 x 8 heads of 128 are
-// 202 MB, 31 us at the measured copy rate, and take 41), latency for a decode step (4 us for 32 tokens).
+// 202 MB, 31 us at the measured copy rate, and take 40.5), latency for a decode step (3.9 us for 32 tokens).
 // A warp's loads of eight rounds (32 rows) are in flight together while it looks up the token, its page
 // and its angles; four rounds a warp took 44.5 us, six 42.6, ten 44.1, twelve 50.2.  Of int8, whose rounds
-// hold their rows' ranges and codes as well, 1005 tokens took 27 us with their gather at three rounds, 29 at
-// two and four, 30 at six.
+// hold their rows' ranges and codes as well, 1005 tokens of 3 x 32 heads took 27 us with their gather at three
+// rounds, 29 at two and four, 30 at six; of the 27 the append takes 22.5 (16 bits: 15.0), the gather 5.7 (4.8).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -223,7 +223,7 @@ __device__ void bounds_in_call(const KvAppendParams& p, uint8_t* page, int g, in
 constexpr int append_ctas(bool bounds, int rounds) { return rounds > 4 || bounds ? 2 : rounds > 2 ? 3 : 4; }
 
 // One warp per task of ROUNDS rounds of a token's rows, their loads in flight together (`slices` tasks a
-// token), the tasks in turn where there are more than warps (42.6 us instead of 44.5 for 8192 tokens); behind
+// token), the tasks in turn where there are more than warps (40.6 us for 8192 tokens; a warp per task 45.9); behind
 // them, with BOUNDS, D / 64 warps per (token, KV head) that do something where the token completes its page.
 template <int FMT, int D, bool BOUNDS, int ROUNDS>
 __global__ void __launch_bounds__(32 * kAppendWarps, append_ctas(BOUNDS, ROUNDS))
@@ -463,7 +463,10 @@ cudaError_t append_launch(const KvAppendParams& p, cudaStream_t s) {
   // Few tokens: the bounds in the same launch, where a completed page's warps look through the call's
   // tokens.  More: a launch behind it.  One launch and two took 2.8 and 4.7 us for 32 bf16 tokens of one
   // sequence, 4.1 and 6 for 32 sequences that all complete a page, but 7.3 and 5.8 for 64 of one sequence,
-  // whose keys each of those warps makes again.
+  // whose keys each of those warps makes again.  The host sees the number of tokens, not whose they are: steps
+  // of more sequences pay for that rule.  Of 64 and 256 sequences with one token each, one launch and two took
+  // 3.2 and 5.0, 3.6 and 5.3 where none completes a page, 4.0 and 6.1, 6.1 and 6.3 where one in 64 does, 4.7 and 7.0,
+  // 10.5 and 12.1 where all do.
   if (p.n_tok <= kFusedBoundsMax) return append_rounds<FMT, D, true, 2>(p, s);
   const cudaError_t e = append_rounds<FMT, D, false, FMT == STARKV_KV_INT8 ? kRoundsInt8 : kRounds16>(p, s);
   if (e != cudaSuccess) return e;

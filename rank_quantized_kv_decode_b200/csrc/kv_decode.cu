@@ -5,12 +5,13 @@
 // fp32; raising m multiplies l and O by 2^{m_old - m_new}.  Parts of a sequence join by
 // M = max m_i, l = sum l_i 2^{m_i - M}, O likewise.
 //
-// Bound: HBM.  Every byte of the visited keys and values is read once (for up to eight query heads
-// per KV head), 4 FLOP per byte and query head at 16 bits; the products run on mma.sync
-// m16n8k16, whose 16 rows hold the query heads in the upper half.  For P.V the lower half holds what the
-// weights lost in rounding to 16 bits (p = hi + lo), so that the weights count with 16 bits of mantissa
-// (bf16) or 22 (fp16) at no further instruction.  tcgen05 would give the same products of 8 rows a
-// 128-row tile.
+// Bound: HBM.  Every byte of the visited keys and values is read once for each eight query heads of a KV
+// head: a ninth makes the list twice as long (8 x 32768 bf16 tokens, d 128: 32 query over 4 KV heads take
+// 96 us, 64 over 4 163; 64 over 8 174, 128 over 8 308).  4 FLOP per byte and query head at 16 bits; the
+// products run on mma.sync m16n8k16, whose 16 rows hold the query heads in the upper half.  For P.V the
+// lower half holds what the weights lost in rounding to 16 bits (p = hi + lo), so that the weights count
+// with 16 bits of mantissa (bf16) or 22 (fp16) at no further instruction.  tcgen05 would give the same
+// products of 8 rows a 128-row tile.
 //
 // Split: a warp works alone.  Its unit is a tile of 16 tokens (int8: 32) of one KV head; the tiles of all
 // sequences and KV heads form one list, cut into chunks wherever the sequences begin, and a chunk's part
@@ -25,10 +26,11 @@
 // (TMA copies of the same tiles, issued by one lane: no faster at 32 x 32768 tokens and slower for short
 // ones, 22.1 us against 19.4 at a ragged fp16 batch.)
 //
-// Measured: 7.0 TB/s at 32 x 32768 bf16 tokens with 8 KV heads (612 us), 6.2 at 8 x 4096 with 32 (86 us:
-// 4.6 us until the first tile and 3 of the join count there), 4.3 at 131072 int8 tokens (66 us).  int8 is
-// bound by the warps' own instructions: two warps a scheduler (64 fp32 sums a lane for d 128) at half
-// the issue rate, most of it decoding codes; twelve warps an SM spilled and took 92 us.
+// Measured, in a graph: 6.9 TB/s at 32 x 32768 bf16 tokens with 8 KV heads (621 us), 6.2 at 8 x 4096 with
+// 32 (87 us: 4.6 us until the first tile and 3 of the join count there), 4.4 at 131072 int8 tokens (64.5 us).
+// int8 has no unit near its limit (issue 48 %, DRAM 53 %, tensor pipe 26 %): two warps a scheduler (64 fp32
+// sums a lane for d 128) do not cover one another's latencies while they decode codes; twelve warps an SM
+// spilled and took 92 us.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -38,8 +40,12 @@ namespace {
 
 constexpr float kLazy = 8.f;  // the reference follows the running maximum when that is 2^8 above it:
                               // weights stay below 2^8, and O is rescaled a few times per sequence
-// Tiles a warp from which on some are drawn: at 55 (8 x 4096 tokens, 32 KV heads) drawing took 88.6 us and
-// equal shares 92.8, at 28 (131072 int8 tokens, 8 KV heads) drawing took 91 and equal shares 74.
+// Tiles a warp above which some are drawn.  Drawing pays where the SMs' shares of the memory's rate differ by
+// more than the small chunks cost: 32 x 32768 bf16 tokens (443 tiles a warp) took 612 us with it and 652
+// without, 8 x 4096 with 32 KV heads (55) 88.6 and 92.8.  With d 128 and 8 KV heads in 8 sequences, drawing
+// and equal shares took, in us: bf16 at 28 tiles 53.3 and 50.9, 44: 77.2 and 74.5, 64: 106 and 105, 96: 151 and
+// 151; int8 at 28 70 and 63, 44: 105 and 92, 96: 201 and 184.  One number does not fit them all: 40 lies below the
+// border of those lists.
 constexpr unsigned kStatic = 40;
 constexpr unsigned kDrawnPart = 4;  // one tile in so many is drawn: one in 2, 3, 4 took 634, 626, 621 us at 32 x 32768
 constexpr int kSmall = 8;           // tiles of a drawn chunk at least (4: 92.3 us at 8 x 4096, 8: 90.2); at most
@@ -642,6 +648,7 @@ __device__ __forceinline__ float part_weight(float m, float M) {
 
 
 // Sets the counter of chunks drawn to zero before a split kernel that may draw, whatever the workspace holds.
+// In a graph it adds 0.3 us to 8 x 1000 tokens under a block table of 2048 pages (11.6 us), outside 1 us.
 __global__ void kv_counter_kernel(unsigned* counter) {
   pdl_launch_dependents();
   pdl_wait();

@@ -14,9 +14,10 @@
 // largest bit by bit 4 us of a sequence's 17, the histogram 1.
 //
 // Bound: HBM for large batches (the bounds are 4 d bytes per page and KV head, read once), latency
-// for one sequence.  32 sequences x 512 pages x 8 KV heads take 26 us (67 MB, 10 us at the measured copy
-// rate): 14 until all is scored, then 6 for the choice; one sequence of 2047 pages 12.5.  Bounds through a
-// cp.async ring, always two rounds in flight, scored no faster (26 to 30 us).  A cluster of CTAs shares one
+// for one sequence.  32 sequences x 512 pages x 8 KV heads take 25.4 us in a graph (67 MB, 10 us at the
+// measured copy rate; 24.5 where they are in L2 already): 14 until all is scored, then 6 for the choice; one
+// sequence of 2047 pages 12.5.  Bounds through a cp.async ring, always two rounds in flight, scored no faster
+// (26 to 30 us).  A cluster of CTAs shares one
 // (sequence, KV head): each scores its share of the pages into the first CTA's shared memory, which then
 // chooses.
 #include <cooperative_groups.h>
